@@ -10,6 +10,9 @@ LIB_PATH = os.path.join(_PKG, "librglru.so")
 RGLRU_F32 = 0
 RGLRU_BF16 = 1
 
+RGLRU_GELU = 0
+RGLRU_SILU = 1
+
 STATUS = {
     0: "RGLRU_OK", -1: "RGLRU_ERR_NULL", -2: "RGLRU_ERR_SHAPE", -3: "RGLRU_ERR_ALIGN", -4: "RGLRU_ERR_DTYPE",
     -5: "RGLRU_ERR_WORKSPACE", -6: "RGLRU_ERR_CUDA", -7: "RGLRU_ERR_TIMEOUT", -8: "RGLRU_ERR_DEVICE",
@@ -95,6 +98,15 @@ SIGNATURES = {
     "rglru_backward_saved": (_I, [_PP, _P, _P, _P, _P, _P, _P, _P, _GP, _I, _I, _I, _P, _S, _P]),
     "rglru_gate_scan_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "rglru_gate_scan": (_I, [_PP, _P, _P, _P, _P, _I, _I, _I, _I, _P, _S, _P]),
+    "rglru_glu_forward": (_I, [_P, _P, _P, _P, _L, _I, _I, _I, _P]),
+    "rglru_glu_backward_workspace_bytes": (_S, [_L, _I, _I, _I]),
+    "rglru_glu_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _P, _S, _P]),
+    "rglru_glu_backward_act8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _P, _S, _P]),
+    "rglru_act8_pack": (_I, [_P, _P, _P, _L, _I, _I, _P]),
+    "rglru_act8_unpack": (_I, [_P, _P, _P, _L, _I, _I, _P]),
+    "rglru_w4_quantize": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "rglru_w4_linear": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "rglru_w4_glu": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "rglru_workspace_status": (_I, [_P, _P]),
     "rglru_strerror": (ctypes.c_char_p, [_I]),
     "rglru_last_cuda_error": (_I, []),

@@ -73,6 +73,10 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn get_encode_tiled();
+// Tensor map of a bf16 matrix [outer][inner] with rows of row_bytes, boxes box_outer × box_inner,
+// 128-byte swizzle; elements outside the matrix read as zero. False if it cannot be encoded.
+bool make_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                 uint32_t box_inner, uint32_t box_outer);
 int num_sms();
 
 // `status`: device word the kernel ORs kStatusTimeout into if a bounded wait gives up.
@@ -206,5 +210,46 @@ struct BwdArgs {
   int B, T, R;
 };
 cudaError_t launch_backward(const BwdArgs& g, const BwdLayout& L, void* ws, cudaStream_t s);
+
+// ---- the gated feed-forward block (glu.cu) and its compressed forms (act8.cu, w4.cu) --------
+// h = act(x W_gateᵀ) ⊙ (x W_upᵀ): x [N][D], W_gate, W_up [H][D], h [N][H] bf16; act: kActGelu or
+// kActSilu (act_math.cuh).
+cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
+                               int act, unsigned* status, cudaStream_t s);
+struct GluBwdArgs {
+  const void* W_gate;  // [H][D]
+  const void* W_up;
+  const void* x;       // [N][D]
+  const void* dh;      // [N][H]
+  void* dg;            // [N][H] scratch
+  void* du;            // [N][H] scratch
+  void* dx;            // [N][D]
+  void* dW_gate;       // [H][D]
+  void* dW_up;
+  void* h;             // [N][H], or null
+  int64_t N;
+  int D, H, act;
+};
+cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStream_t s);
+// x [rows][C] (bf16 or float32) ↔ int8 codes [rows][C] and scale bytes [rows][⌈C/32⌉]; C a
+// multiple of 8.
+constexpr int kAct8Group = 32;
+cudaError_t launch_act8_pack(const void* x, void* codes, void* scales, int64_t rows, int C, bool bf16,
+                             cudaStream_t s);
+cudaError_t launch_act8_unpack(const void* codes, const void* scales, void* x, int64_t rows, int C, bool bf16,
+                               cudaStream_t s);
+// 4-bit weights: codes [rows][K/2], scales [rows][K/group] bf16; group 32, 64 or 128 divides K,
+// rows a multiple of 8, 1 ≤ M ≤ kW4MaxTokens.
+constexpr int kW4MaxTokens = 64;
+struct W4Matrix {
+  const void* codes;
+  const void* scales;
+};
+cudaError_t launch_w4_quantize(const void* w, void* codes, void* scales, int64_t rows, int K, int group,
+                               cudaStream_t s);
+cudaError_t launch_w4_linear(const W4Matrix& w, const void* x, void* y, int M, int rows, int K, int group,
+                             cudaStream_t s);
+cudaError_t launch_w4_glu(const W4Matrix& gate, const W4Matrix& up, const void* x, void* h, int M, int rows, int K,
+                          int group, int act, cudaStream_t s);
 
 }  // namespace rglru

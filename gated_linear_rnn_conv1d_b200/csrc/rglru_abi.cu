@@ -8,6 +8,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/rglru.h"
+#include "act_math.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -922,6 +923,170 @@ int rglru_attention_layer_step(const rglru_attention_layer_weights* w, const voi
   if (e == cudaSuccess) e = launch_gelu_mul(gate, up, gate, (int64_t)B * H, s);
   if (e == cudaSuccess) e = launch_gemm_bf16(gate, w->W_down, o, B, D, H, D, status, s);
   if (e == cudaSuccess) e = launch_add_rmsnorm(res, o, out_t, nullptr, nullptr, B, D, eps, s);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+// ---- the gated feed-forward block, 8-bit checkpoints, 4-bit weights --------------------------
+namespace {
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+static_assert(RGLRU_GELU == kActGelu && RGLRU_SILU == kActSilu, "activation codes");
+bool valid_glu(int64_t N, int D, int H, int act) {
+  // (tile counts and tile rows stay in 32 bits)
+  return N >= 1 && N <= kMaxTokens && valid_R(D) && valid_R(H) && (act == kActGelu || act == kActSilu) &&
+         ((N + 255) / 256) * (((D > H ? D : H) + 127) / 128) <= kMaxTokens;
+}
+bool valid_act8(int64_t N, int C) {
+  return N >= 1 && N <= kMaxTokens && valid_R(C) && N * ((C + kAct8Group - 1) / kAct8Group) <= (int64_t)INT32_MAX * 64;
+}
+bool valid_w4(int N, int K, int group) {
+  return valid_R(N) && valid_R(K) && (group == 32 || group == 64 || group == 128) && K % group == 0;
+}
+// dg [N][H] | du [N][H] | x̂ [N][D] (from_act8), bf16
+struct GluBwdLayout {
+  size_t off_du, off_x, bytes;
+};
+GluBwdLayout glu_bwd_layout(int64_t N, int D, int H, bool from_act8) {
+  GluBwdLayout L;
+  L.off_du = round256((size_t)N * H * 2);
+  L.off_x = 2 * L.off_du;
+  L.bytes = L.off_x + (from_act8 ? round256((size_t)N * D * 2) : 0);
+  return L;
+}
+int glu_backward_impl(const void* W_gate, const void* W_up, const void* x, const void* codes, const void* scales,
+                      const void* dh, void* dx, void* dW_gate, void* dW_up, void* h, int64_t N, int D, int H,
+                      int act, void* workspace, size_t workspace_bytes, rglru_stream_t stream) {
+  const bool from_act8 = x == nullptr;
+  if (!valid_glu(N, D, H, act) || (from_act8 && !valid_act8(N, D))) return RGLRU_ERR_SHAPE;
+  if (W_gate == nullptr || W_up == nullptr || (from_act8 && (codes == nullptr || scales == nullptr)) ||
+      dh == nullptr || dx == nullptr || dW_gate == nullptr || dW_up == nullptr)
+    return RGLRU_ERR_NULL;
+  if (!aligned16(W_gate) || !aligned16(W_up) || !aligned16(x) || !aligned16(codes) || !aligned16(scales) ||
+      !aligned16(dh) || !aligned16(dx) || !aligned16(dW_gate) || !aligned16(dW_up) || !aligned16(h))
+    return RGLRU_ERR_ALIGN;
+  const GluBwdLayout L = glu_bwd_layout(N, D, H, from_act8);
+  if (workspace == nullptr || workspace_bytes < L.bytes) return RGLRU_ERR_WORKSPACE;
+  if (!aligned256(workspace)) return RGLRU_ERR_ALIGN;
+  int st = check_device();
+  if (st != RGLRU_OK) return st;
+  unsigned* status = global_status_word();
+  if (status == nullptr) return fail_cuda(cudaGetLastError());
+  cudaStream_t s = (cudaStream_t)stream;
+  if (from_act8) {
+    void* xhat = bytes(workspace) + L.off_x;
+    cudaError_t e = launch_act8_unpack(codes, scales, xhat, N, D, true, s);
+    if (e != cudaSuccess) return fail_cuda(e);
+    x = xhat;
+  }
+  GluBwdArgs b{};
+  b.W_gate = W_gate; b.W_up = W_up; b.x = x; b.dh = dh;
+  b.dg = workspace; b.du = bytes(workspace) + L.off_du;
+  b.dx = dx; b.dW_gate = dW_gate; b.dW_up = dW_up; b.h = h;
+  b.N = N; b.D = D; b.H = H; b.act = act;
+  const cudaError_t e = launch_glu_backward(b, status, s);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+}  // namespace
+
+int rglru_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
+                      int activation, rglru_stream_t stream) {
+  const Range range("rglru_glu_forward");
+  if (!valid_glu(N, D, H, activation)) return RGLRU_ERR_SHAPE;
+  if (W_gate == nullptr || W_up == nullptr || x == nullptr || h == nullptr) return RGLRU_ERR_NULL;
+  if (!aligned16(W_gate) || !aligned16(W_up) || !aligned16(x) || !aligned16(h)) return RGLRU_ERR_ALIGN;
+  int st = check_device();
+  if (st != RGLRU_OK) return st;
+  unsigned* status = global_status_word();
+  if (status == nullptr) return fail_cuda(cudaGetLastError());
+  const cudaError_t e = launch_glu_forward(W_gate, W_up, x, h, N, D, H, activation, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+size_t rglru_glu_backward_workspace_bytes(int64_t N, int D, int H, int from_act8) {
+  if (!valid_glu(N, D, H, kActGelu) || (from_act8 && !valid_act8(N, D))) return 0;
+  return glu_bwd_layout(N, D, H, from_act8 != 0).bytes;
+}
+
+int rglru_glu_backward(const void* W_gate, const void* W_up, const void* x, const void* dh, void* dx, void* dW_gate,
+                       void* dW_up, void* h, int64_t N, int D, int H, int activation, void* workspace,
+                       size_t workspace_bytes, rglru_stream_t stream) {
+  const Range range("rglru_glu_backward");
+  if (!valid_glu(N, D, H, activation)) return RGLRU_ERR_SHAPE;
+  if (x == nullptr) return RGLRU_ERR_NULL;
+  return glu_backward_impl(W_gate, W_up, x, nullptr, nullptr, dh, dx, dW_gate, dW_up, h, N, D, H, activation,
+                           workspace, workspace_bytes, stream);
+}
+
+int rglru_glu_backward_act8(const void* W_gate, const void* W_up, const void* codes, const void* scales,
+                            const void* dh, void* dx, void* dW_gate, void* dW_up, void* h, int64_t N, int D, int H,
+                            int activation, void* workspace, size_t workspace_bytes, rglru_stream_t stream) {
+  const Range range("rglru_glu_backward_act8");
+  return glu_backward_impl(W_gate, W_up, nullptr, codes, scales, dh, dx, dW_gate, dW_up, h, N, D, H, activation,
+                           workspace, workspace_bytes, stream);
+}
+
+int rglru_act8_pack(const void* x, void* codes, void* scales, int64_t N, int C, int io_dtype, rglru_stream_t stream) {
+  const Range range("rglru_act8_pack");
+  if (!valid_dtype(io_dtype)) return RGLRU_ERR_DTYPE;
+  if (!valid_act8(N, C)) return RGLRU_ERR_SHAPE;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const int st = check_device();
+  if (st != RGLRU_OK) return st;
+  const cudaError_t e = launch_act8_pack(x, codes, scales, N, C, io_dtype == RGLRU_BF16, (cudaStream_t)stream);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+int rglru_act8_unpack(const void* codes, const void* scales, void* x, int64_t N, int C, int io_dtype,
+                      rglru_stream_t stream) {
+  const Range range("rglru_act8_unpack");
+  if (!valid_dtype(io_dtype)) return RGLRU_ERR_DTYPE;
+  if (!valid_act8(N, C)) return RGLRU_ERR_SHAPE;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const int st = check_device();
+  if (st != RGLRU_OK) return st;
+  const cudaError_t e = launch_act8_unpack(codes, scales, x, N, C, io_dtype == RGLRU_BF16, (cudaStream_t)stream);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+int rglru_w4_quantize(const void* W, void* codes, void* scales, int N, int K, int group, rglru_stream_t stream) {
+  const Range range("rglru_w4_quantize");
+  if (!valid_w4(N, K, group)) return RGLRU_ERR_SHAPE;
+  if (W == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
+  if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const int st = check_device();
+  if (st != RGLRU_OK) return st;
+  const cudaError_t e = launch_w4_quantize(W, codes, scales, N, K, group, (cudaStream_t)stream);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+int rglru_w4_linear(const void* codes, const void* scales, const void* x, void* y, int M, int N, int K, int group,
+                    rglru_stream_t stream) {
+  const Range range("rglru_w4_linear");
+  if (!valid_w4(N, K, group) || M < 1 || M > kW4MaxTokens) return RGLRU_ERR_SHAPE;
+  if (codes == nullptr || scales == nullptr || x == nullptr || y == nullptr) return RGLRU_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(x) || !aligned16(y)) return RGLRU_ERR_ALIGN;
+  const int st = check_device();
+  if (st != RGLRU_OK) return st;
+  const cudaError_t e = launch_w4_linear({codes, scales}, x, y, M, N, K, group, (cudaStream_t)stream);
+  return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
+}
+
+int rglru_w4_glu(const void* gate_codes, const void* gate_scales, const void* up_codes, const void* up_scales,
+                 const void* x, void* h, int M, int H, int D, int group, int activation, rglru_stream_t stream) {
+  const Range range("rglru_w4_glu");
+  if (!valid_w4(H, D, group) || M < 1 || M > kW4MaxTokens || (activation != kActGelu && activation != kActSilu))
+    return RGLRU_ERR_SHAPE;
+  if (gate_codes == nullptr || gate_scales == nullptr || up_codes == nullptr || up_scales == nullptr ||
+      x == nullptr || h == nullptr)
+    return RGLRU_ERR_NULL;
+  if (!aligned16(gate_codes) || !aligned16(gate_scales) || !aligned16(up_codes) || !aligned16(up_scales) ||
+      !aligned16(x) || !aligned16(h))
+    return RGLRU_ERR_ALIGN;
+  const int st = check_device();
+  if (st != RGLRU_OK) return st;
+  const cudaError_t e = launch_w4_glu({gate_codes, gate_scales}, {up_codes, up_scales}, x, h, M, H, D, group,
+                                      activation, (cudaStream_t)stream);
   return e == cudaSuccess ? RGLRU_OK : fail_cuda(e);
 }
 

@@ -438,6 +438,84 @@ RGLRU_API int rglru_gate_scan(const rglru_params* params, const void* u, const f
 RGLRU_API int rglru_gemm_bf16(const void* A, const void* Bm, void* C, int64_t M, int N, int K, rglru_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * The gated feed-forward block ("Griffin：…", §MLP块 (gated MLP, Fig. 2(b))) without its down
+ * projection, for training and serving:
+ *     h = act(x W_gateᵀ) ⊙ (x W_upᵀ)
+ * in one kernel; both products stay on the chip in float32 until h is rounded to bf16, once. (The
+ * Hawk layer's calls above keep their own sequence of kernels and roundings.)
+ *   x             [N][D] bf16 (N tokens, any batch and time shape)
+ *   W_gate, W_up  [H][D] bf16, row-major [out][in]
+ *   h             [N][H] bf16
+ *   activation    RGLRU_GELU (g·Φ(g)) or RGLRU_SILU (g·σ(g))
+ * 1 ≤ N ≤ 2^30; D, H multiples of 8 up to 65536; ⌈N/256⌉·⌈max(D, H)/128⌉ ≤ 2^30
+ * (RGLRU_ERR_SHAPE otherwise, and for an unknown activation). No workspace: a timeout of a
+ * bounded wait of any call of this section is reported by rglru_workspace_status(NULL, stream).
+ *
+ * rglru_glu_backward: the gradients of a scalar loss ℓ given dh = ∂ℓ/∂h, with
+ * g = x W_gateᵀ and u = x W_upᵀ formed again from x (nothing of the forward is kept but x):
+ *     dg = dh ⊙ u ⊙ act'(g),  du = dh ⊙ act(g),
+ *     dx = dg W_gate + du W_up,  dW_gate = dgᵀ x,  dW_up = duᵀ x.
+ *   dh [N][H], dx [N][D], dW_gate and dW_up [H][D]: bf16, sums in float32
+ *   h             [N][H] bf16 or NULL: the forward's h again, for the down projection's gradient
+ *   workspace     at least rglru_glu_backward_workspace_bytes(N, D, H, 0) bytes, 256-byte aligned
+ *                 (dg and du in bf16); it needs no initialisation
+ * rglru_glu_backward_act8: the same, x given as its 8-bit checkpoint (rglru_act8_pack): the
+ *   gradients at x̂, which the tensor cores read without a further rounding. workspace: at least
+ *   rglru_glu_backward_workspace_bytes(N, D, H, 1) bytes.
+ * Results are deterministic: no atomics.
+ * --------------------------------------------------------------------------------- */
+typedef enum { RGLRU_GELU = 0, RGLRU_SILU = 1 } rglru_activation;
+RGLRU_API int rglru_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
+                                int activation, rglru_stream_t stream);
+RGLRU_API size_t rglru_glu_backward_workspace_bytes(int64_t N, int D, int H, int from_act8);
+RGLRU_API int rglru_glu_backward(const void* W_gate, const void* W_up, const void* x, const void* dh, void* dx,
+                                 void* dW_gate, void* dW_up, void* h, int64_t N, int D, int H, int activation,
+                                 void* workspace, size_t workspace_bytes, rglru_stream_t stream);
+RGLRU_API int rglru_glu_backward_act8(const void* W_gate, const void* W_up, const void* codes, const void* scales,
+                                      const void* dh, void* dx, void* dW_gate, void* dW_up, void* h, int64_t N, int D,
+                                      int H, int activation, void* workspace, size_t workspace_bytes,
+                                      rglru_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits: what a backward pass needs of an activation, in 33/32 bytes
+ * a value. Each row's channels form groups of 32 (the last may be short); a group with largest
+ * magnitude m is held as int8 codes and one power of two,
+ *     e = the smallest integer ≥ −127 with |rint(x / 2^e)| ≤ 127,  code = rint(x / 2^e),
+ *     x̂ = code · 2^e  (rint to even; |x̂ − x| ≤ 2^(e−1) ≤ m / 127 for m ≥ 2^-121).
+ * x̂ is a bfloat16 number, so unpacking rounds nothing in either type. A group that holds an
+ * infinity or a NaN comes back as NaN.
+ *   x       [N][C] io_dtype
+ *   codes   [N][C] int8
+ *   scales  [N][⌈C/32⌉] bytes: e + 127 (0 … 249), or 255 for a group that is not finite
+ * 1 ≤ N ≤ 2^30, C a multiple of 8 up to 65536.
+ * --------------------------------------------------------------------------------- */
+RGLRU_API int rglru_act8_pack(const void* x, void* codes, void* scales, int64_t N, int C, int io_dtype,
+                              rglru_stream_t stream);
+RGLRU_API int rglru_act8_unpack(const void* codes, const void* scales, void* x, int64_t N, int C, int io_dtype,
+                                rglru_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * Linears with 4-bit weights for a few tokens (decode: the weights' bytes are what a step costs):
+ *     y = x Ŵᵀ,  h = act(x Ŵ_gateᵀ) ⊙ (x Ŵ_upᵀ),  Ŵ[n][k] = s[n][k / group]·(q[n][k] − 8)
+ *   codes   [N][K/2] bytes: q[n][2j] in the low and q[n][2j + 1] in the high four bits of byte j
+ *   scales  [N][K/group] bf16
+ *   x       [M][K] bf16, 1 ≤ M ≤ 64;  y [M][N] (h [M][H]) bf16
+ *   group   32, 64 or 128 inputs, a divisor of K
+ * N (H) and K (D) multiples of 8 up to 65536 (RGLRU_ERR_SHAPE otherwise). Sums are float32; y is
+ * rounded once.
+ * rglru_w4_quantize forms codes and scales from a bf16 matrix W [N][K]: s = bf16(max |w| / 7) of
+ * the group, q = rint(w / s) + 8 within 1 … 15 (divisions in float32, rint to even); zeros give
+ * s = 0 and q = 8, a group with an infinity or a NaN s = NaN and q = 8.
+ * --------------------------------------------------------------------------------- */
+RGLRU_API int rglru_w4_quantize(const void* W, void* codes, void* scales, int N, int K, int group,
+                                rglru_stream_t stream);
+RGLRU_API int rglru_w4_linear(const void* codes, const void* scales, const void* x, void* y, int M, int N, int K,
+                              int group, rglru_stream_t stream);
+RGLRU_API int rglru_w4_glu(const void* gate_codes, const void* gate_scales, const void* up_codes,
+                           const void* up_scales, const void* x, void* h, int M, int H, int D, int group,
+                           int activation, rglru_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * Status and diagnostics
  * --------------------------------------------------------------------------------- */
 /* Synchronises `stream`, reads and clears the device status word that kernels using

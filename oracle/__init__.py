@@ -12,3 +12,4 @@ from .local_attention import (  # noqa: F401
     ROPE_BASE, WINDOW, rope, local_mqa, local_attention, local_attention_step, griffin_attention_layer,
     griffin_attention_layer_step,
 )
+from . import feed_forward  # noqa: F401

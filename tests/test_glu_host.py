@@ -1,0 +1,93 @@
+"""Refusals of the gated feed-forward block, the 8-bit checkpoints and the 4-bit linears: the library's
+argument checks (nothing is launched, so no GPU is needed) and the binding's."""
+import ctypes
+
+import pytest
+import torch
+
+from gated_linear_rnn_conv1d_b200 import _abi, rglru
+
+OK = ctypes.c_void_p(0x100000)
+WS = ctypes.c_void_p(0x200000)
+ODD = ctypes.c_void_p(0x100008)
+
+
+def test_glu_forward_refusals():
+    f = _abi.load().rglru_glu_forward
+    call = lambda wg=OK, wu=OK, x=OK, h=OK, N=4, D=64, H=72, act=0: f(wg, wu, x, h, N, D, H, act, None)
+    for bad in (dict(N=0), dict(N=-1), dict(N=(1 << 30) + 1), dict(D=0), dict(D=12), dict(D=65544), dict(H=4),
+                dict(H=100), dict(act=2), dict(act=-1), dict(N=1 << 30, H=65536)):
+        assert call(**bad) == -2, bad
+    for k in ("wg", "wu", "x", "h"):
+        assert call(**{k: None}) == -1, k
+        assert call(**{k: ODD}) == -3, k
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_glu_backward_refusals(packed):
+    lib = _abi.load()
+    need = lib.rglru_glu_backward_workspace_bytes(4, 64, 72, int(packed))
+    # dg and du, and x̂ for the packed form, each rounded up to 256 bytes
+    assert need == 2 * 768 + (512 if packed else 0)
+    assert lib.rglru_glu_backward_workspace_bytes(0, 64, 72, 0) == 0
+    assert lib.rglru_glu_backward_workspace_bytes(4, 60, 72, 0) == 0
+
+    def call(wg=OK, wu=OK, x=OK, scales=OK, dh=OK, dx=OK, dwg=OK, dwu=OK, h=None, N=4, D=64, H=72, act=1, ws=WS,
+             wsb=need):
+        if packed:
+            return lib.rglru_glu_backward_act8(wg, wu, x, scales, dh, dx, dwg, dwu, h, N, D, H, act, ws, wsb, None)
+        return lib.rglru_glu_backward(wg, wu, x, dh, dx, dwg, dwu, h, N, D, H, act, ws, wsb, None)
+
+    for bad in (dict(N=0), dict(D=20), dict(H=0), dict(act=3)):
+        assert call(**bad) == -2, bad
+    names = ["wg", "wu", "x", "dh", "dx", "dwg", "dwu"] + (["scales"] if packed else [])
+    for k in names:
+        assert call(**{k: None}) == -1, k
+        assert call(**{k: ODD}) == -3, k
+    assert call(h=ODD) == -3
+    assert call(ws=None) == -5
+    assert call(wsb=need - 1) == -5
+    assert call(ws=ctypes.c_void_p(0x200010)) == -3
+
+
+def test_act8_refusals():
+    lib = _abi.load()
+    for f in (lib.rglru_act8_pack, lib.rglru_act8_unpack):
+        call = lambda a=OK, b=OK, c=OK, N=3, C=40, io=1: f(a, b, c, N, C, io, None)
+        assert call(io=2) == -4
+        for bad in (dict(N=0), dict(C=0), dict(C=36), dict(C=65544), dict(N=(1 << 30) + 1), dict(N=1 << 30, C=65536)):
+            assert call(**bad) == -2, bad
+        for k in ("a", "b", "c"):
+            assert call(**{k: None}) == -1, k
+            assert call(**{k: ODD}) == -3, k
+
+
+def test_w4_refusals():
+    lib = _abi.load()
+    q = lambda a=OK, b=OK, c=OK, N=16, K=256, group=64: lib.rglru_w4_quantize(a, b, c, N, K, group, None)
+    lin = lambda a=OK, b=OK, x=OK, y=OK, M=1, N=16, K=256, group=64: lib.rglru_w4_linear(a, b, x, y, M, N, K, group, None)
+    glu = lambda a=OK, b=OK, c=OK, d=OK, x=OK, h=OK, M=1, N=16, K=256, group=64, act=0: lib.rglru_w4_glu(
+        a, b, c, d, x, h, M, N, K, group, act, None)
+    for f, ptrs in ((q, "abc"), (lin, "abxy"), (glu, "abcdxh")):
+        for bad in (dict(N=0), dict(N=12), dict(K=0), dict(K=96), dict(group=16), dict(group=256), dict(group=0),
+                    dict(K=160, group=128)):
+            assert f(**bad) == -2, bad
+        for k in ptrs:
+            assert f(**{k: None}) == -1, k
+            assert f(**{k: ODD}) == -3, k
+        if f is not q:
+            assert f(M=0) == -2 and f(M=65) == -2
+    assert glu(act=2) == -2
+
+
+def test_binding_takes_cuda_tensors_only():
+    b = torch.bfloat16
+    w, x, dh = torch.zeros(72, 64, dtype=b), torch.zeros(3, 64, dtype=b), torch.zeros(3, 72, dtype=b)
+    a8 = rglru.Act8(torch.zeros(3, 64, dtype=torch.int8), torch.zeros(3, 2, dtype=torch.uint8), b)
+    w4 = rglru.W4Weight(torch.zeros(72, 32, dtype=torch.uint8), torch.zeros(72, 1, dtype=b), 64)
+    for call in (lambda: rglru.glu_forward(w, w, x), lambda: rglru.glu_backward(w, w, x, dh),
+                 lambda: rglru.glu_backward(w, w, a8, dh), lambda: rglru.act8_pack(x), lambda: rglru.act8_unpack(a8),
+                 lambda: rglru.w4_quantize(w, 64), lambda: rglru.w4_linear(w4, x),
+                 lambda: rglru.w4_glu(w4, w4, x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

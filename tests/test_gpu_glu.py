@@ -1,0 +1,225 @@
+"""The gated feed-forward block on the GPU, forward and backward, against the float64 oracle; the bounds are
+derived in _glu.py."""
+import numpy as np
+import pytest
+import torch
+
+from gated_linear_rnn_conv1d_b200 import rglru
+from oracle import feed_forward as ff
+
+from _glu import backward_bounds, forward_bound
+from _util import f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def _draw(N, D, H, seed=0, scale=1.0):
+    g = torch.Generator("cpu").manual_seed(1000 + seed)
+    x = torch.randn(N, D, generator=g).to(BF)
+    Wg = (torch.randn(H, D, generator=g) * (scale / D ** 0.5)).to(BF)
+    Wu = (torch.randn(H, D, generator=g) / D ** 0.5).to(BF)
+    dh = torch.randn(N, H, generator=g).to(BF)
+    return x, Wg, Wu, dh
+
+
+def _guarded(shape, dtype=BF):
+    """A tensor of that shape inside a larger buffer of a known pattern, and a check that the rest of it is
+    as it was."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2048,), -7.0, dtype=dtype, device=DEV)
+    view = buf[1024:1024 + n].view(shape)
+
+    def untouched():
+        return bool((buf[:1024] == -7.0).all() and (buf[1024 + n:] == -7.0).all())
+
+    return view, untouched
+
+
+def _check_forward(x, Wg, Wu, act, h):
+    ref = ff.glu_forward(f64(x), f64(Wg), f64(Wu), act)
+    bound = forward_bound(f64(x), f64(Wg), f64(Wu), lambda g: ff.act(g, act), ref)
+    err = np.abs(f64(h) - ref)
+    print(f"worst error / bound {np.max(err / bound):.3f}")
+    assert (err <= bound).all()
+
+
+def _check_backward(x, Wg, Wu, dh, act, got):
+    X, G, U, DH = f64(x), f64(Wg), f64(Wu), f64(dh)
+    ref = ff.glu_backward(X, G, U, DH, act)
+    bounds = backward_bounds(X, G, U, DH, lambda g: ff.act(g, act), lambda g: ff.act_slope(g, act))
+    bounds["h"] = forward_bound(X, G, U, lambda g: ff.act(g, act), ref["h"])
+    for k, b in bounds.items():
+        if got[k] is None:
+            continue
+        err = np.abs(f64(got[k]) - ref[k])
+        print(f"{k}: worst error / bound {np.max(err / b):.3f}")
+        assert (err <= b).all(), k
+
+
+# one token; one over a vector, a tile and a pair of tiles; widths below, at and past the tiles' 64,
+# 128 and 256; several tiles a CTA pair (9 × 21 tiles on 74 pairs)
+SHAPES = [(1, 8, 8), (1, 264, 776), (2, 72, 136), (3, 512, 128), (5, 1032, 264), (8, 256, 1000), (9, 136, 72),
+          (16, 264, 520), (17, 64, 264), (33, 520, 136), (64, 128, 256), (65, 264, 264), (129, 72, 520),
+          (256, 264, 136), (257, 328, 392), (513, 136, 264), (2100, 72, 2600)]
+
+
+@pytest.mark.parametrize("N,D,H", SHAPES)
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_forward(N, D, H, act):
+    x, Wg, Wu, _ = _draw(N, D, H, seed=N)
+    h, untouched = _guarded((N, H))
+    out = rglru.glu_forward(Wg.to(DEV), Wu.to(DEV), x.to(DEV), activation=act, h=h)
+    assert rglru.workspace_status(None) == 0
+    assert out is h and untouched()
+    _check_forward(x, Wg, Wu, act, h)
+
+
+@pytest.mark.parametrize("N,D,H", SHAPES)
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_backward(N, D, H, act):
+    x, Wg, Wu, dh = _draw(N, D, H, seed=N + 7)
+    # the workspace's old contents are NaN in bf16 and must not be read
+    ws = torch.full((rglru.glu_backward_workspace_bytes(N, D, H),), 0xFF, dtype=torch.uint8, device=DEV)
+    got = rglru.glu_backward(Wg.to(DEV), Wu.to(DEV), x.to(DEV), dh.to(DEV), activation=act, want_h=True, workspace=ws)
+    assert rglru.workspace_status(None) == 0
+    _check_backward(x, Wg, Wu, dh, act, got)
+
+
+def test_shapes_of_any_rank():
+    x, Wg, Wu, dh = _draw(6, 40, 72)
+    w = (Wg.to(DEV), Wu.to(DEV))
+    flat = rglru.glu_forward(*w, x.to(DEV))
+    back = rglru.glu_backward(*w, x.to(DEV), dh.to(DEV))
+    for lead in ((2, 3), (1, 6, 1)):
+        h = rglru.glu_forward(*w, x.to(DEV).view(*lead, 40))
+        assert h.shape == (*lead, 72) and torch.equal(h.view(6, 72), flat)
+        r = rglru.glu_backward(*w, x.to(DEV).view(*lead, 40), dh.to(DEV).view(*lead, 72))
+        assert r["dx"].shape == (*lead, 40) and r["h"] is None
+        assert all(torch.equal(r[k].view_as(back[k]), back[k]) for k in ("dx", "dW_gate", "dW_up"))
+    one = rglru.glu_forward(*w, x[0].to(DEV))
+    assert one.shape == (72,)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_far_pre_activations(act):
+    """Pre-activations of tens and hundreds: both tails of the activation and its slope."""
+    x, Wg, Wu, dh = _draw(130, 64, 136, seed=3, scale=60.0)
+    w = (Wg.to(DEV), Wu.to(DEV))
+    _check_forward(x, Wg, Wu, act, rglru.glu_forward(*w, x.to(DEV), activation=act))
+    _check_backward(x, Wg, Wu, dh, act, rglru.glu_backward(*w, x.to(DEV), dh.to(DEV), activation=act, want_h=True))
+
+
+@pytest.mark.parametrize("N", [1, 3, 12, 300])
+def test_non_finite_rows_stay_in_their_rows(N):
+    x, Wg, Wu, dh = _draw(N, 72, 136, seed=4)
+    w = (Wg.to(DEV), Wu.to(DEV))
+    clean = rglru.glu_forward(*w, x.to(DEV))
+    r0 = rglru.glu_backward(*w, x.to(DEV), dh.to(DEV))
+    bad = x.clone()
+    bad[N // 2, 5] = float("nan")
+    h = rglru.glu_forward(*w, bad.to(DEV))
+    r = rglru.glu_backward(*w, bad.to(DEV), dh.to(DEV))
+    keep = torch.arange(N) != N // 2
+    assert torch.isnan(h[N // 2]).all() and torch.equal(h[keep], clean[keep])
+    assert torch.isnan(r["dx"][N // 2]).all() and torch.equal(r["dx"][keep], r0["dx"][keep])
+    assert torch.isnan(r["dW_gate"]).all()
+
+
+def test_zero_rows_and_zero_gradients():
+    x, Wg, Wu, dh = _draw(140, 64, 72, seed=5)
+    x[::2] = 0
+    dh[1::2] = 0
+    w = (Wg.to(DEV), Wu.to(DEV))
+    h = rglru.glu_forward(*w, x.to(DEV))
+    assert not h[::2].any()
+    r = rglru.glu_backward(*w, x.to(DEV), dh.to(DEV))
+    assert not r["dx"][1::2].any()
+    # x = 0 gives u = 0 and act(0) = 0: nothing reaches the weights or x
+    assert not r["dx"][::2].any() and not r["dW_gate"].any() and not r["dW_up"].any()
+
+
+def test_gradient_against_differences_of_the_kernel():
+    """Along one direction of x, at float32-sized steps of a bf16 input the loss cannot be differenced
+    finely; a step of 2^-4 of unit inputs with the second-order term cancelled leaves a third-order one."""
+    x, Wg, Wu, dh = _draw(64, 128, 256, seed=6)
+    w = (Wg.to(DEV), Wu.to(DEV))
+    v = torch.randn(64, 128, generator=torch.Generator().manual_seed(9)).sign().to(BF) * 2 ** -4
+    xb = (x * 8).round().clamp(-24, 24) / 8  # so that x ± v are bf16 numbers
+    r = rglru.glu_backward(*w, xb.to(DEV), dh.to(DEV), activation="silu")
+    want = float((f64(r["dx"]) * f64(v)).sum())
+    loss = [float((f64(dh) * f64(rglru.glu_forward(*w, (xb + s * v).to(DEV), activation="silu"))).sum())
+            for s in (1, -1)]
+    num = (loss[0] - loss[1]) / 2
+    # each h is rounded to bf16: N·H independent errors of at most 2^-8 |h|, about 2^-8/√3 each; five of
+    # their standard deviations, and the third-order term, which the float64 oracle gives exactly
+    exact = [float((f64(dh) * ff.glu_forward(f64(xb + s * v), f64(Wg), f64(Wu), "silu")).sum()) for s in (1, -1)]
+    third = abs((exact[0] - exact[1]) / 2 - float((ff.glu_backward(f64(xb), f64(Wg), f64(Wu), f64(dh), "silu")["dx"]
+                                                    * f64(v)).sum()))
+    h = ff.glu_forward(f64(xb), f64(Wg), f64(Wu), "silu")
+    noise = 5 * 2 ** -8 / 3 ** 0.5 * np.sqrt(np.sum((f64(dh) * h) ** 2))
+    slack = 5 * 2 ** -7 / 3 ** 0.5 * np.sqrt(np.sum((f64(r["dx"]) * f64(v)) ** 2))
+    print(num, want, third, noise, slack)
+    assert abs(num - want) <= third + noise + slack
+
+
+@pytest.mark.parametrize("N", [1, 7, 200])
+def test_streams_and_two_calls_at_once(N):
+    x, Wg, Wu, dh = (t.to(DEV) for t in _draw(N, 264, 520, seed=8))
+    want = rglru.glu_forward(Wg, Wu, x), rglru.glu_backward(Wg, Wu, x, dh, want_h=True)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in (a, b):
+            got.append((rglru.glu_forward(Wg, Wu, x, stream=s), rglru.glu_backward(Wg, Wu, x, dh, want_h=True, stream=s)))
+    torch.cuda.synchronize()
+    for h, r in got:
+        assert torch.equal(h, want[0])
+        assert all(torch.equal(r[k], want[1][k]) for k in want[1])
+
+
+@pytest.mark.parametrize("N", [1, 40, 300])
+def test_captured_and_replayed(N):
+    x, Wg, Wu, dh = (t.to(DEV) for t in _draw(N, 136, 264, seed=10))
+    rglru.glu_backward(Wg, Wu, x, dh), rglru.glu_forward(Wg, Wu, x)  # first calls outside the capture
+    torch.cuda.synchronize()
+    xin, din = x.clone(), dh.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h = rglru.glu_forward(Wg, Wu, xin)
+        r = rglru.glu_backward(Wg, Wu, xin, din)
+    for seed in (11, 12):
+        x2, _, _, d2 = (t.to(DEV) for t in _draw(N, 136, 264, seed=seed))
+        xin.copy_(x2)
+        din.copy_(d2)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, rglru.glu_forward(Wg, Wu, x2))
+        want = rglru.glu_backward(Wg, Wu, x2, d2)
+        assert all(torch.equal(r[k], want[k]) for k in ("dx", "dW_gate", "dW_up"))
+    assert rglru.workspace_status(None) == 0
+
+
+def test_binding_refusals():
+    x, Wg, Wu, dh = (t.to(DEV) for t in _draw(6, 64, 72))
+    cases = [
+        (TypeError, lambda: rglru.glu_forward(Wg, Wu, x.float())),
+        (TypeError, lambda: rglru.glu_forward(Wg.float(), Wu, x)),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu[:64].contiguous(), x)),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu, x[:, :56].contiguous())),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu, x.t().contiguous().t())),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu, x, activation="relu")),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu, x, h=torch.empty(6, 64, dtype=BF, device=DEV))),
+        (ValueError, lambda: rglru.glu_forward(Wg, Wu.cpu(), x)),
+        (ValueError, lambda: rglru.glu_backward(Wg, Wu, x, dh[:5].contiguous())),
+        (ValueError, lambda: rglru.glu_backward(Wg, Wu, x, dh, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))),
+        (rglru._abi.RGLRUError, lambda: rglru.glu_forward(Wg, Wu, x[:0])),
+        (rglru._abi.RGLRUError, lambda: rglru.glu_forward(Wg[:, :60].contiguous(), Wu[:, :60].contiguous(),
+                                                          x[:, :60].contiguous())),
+    ]
+    for i, (err, call) in enumerate(cases):
+        with pytest.raises(err):
+            call()
+            raise AssertionError(f"case {i} was taken")

@@ -1,0 +1,172 @@
+"""Linears with 4-bit weights on the GPU against the float64 oracle; the bounds are derived in _glu.py."""
+import numpy as np
+import pytest
+import torch
+
+from gated_linear_rnn_conv1d_b200 import rglru
+from oracle import feed_forward as ff
+
+from _glu import ACT, HALF, TINY, w4_bound
+from _util import f64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def _weight(N, K, group, seed):
+    """Every code, scales over several powers of two."""
+    g = torch.Generator("cpu").manual_seed(seed)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    scales = torch.exp(torch.randn(N, K // group, generator=g)).to(BF) / (8 * K ** 0.5)
+    return rglru.W4Weight(codes.to(DEV), scales.to(BF).to(DEV), group)
+
+
+def _dense(w):
+    return ff.w4_dequantize(w.codes.cpu().numpy(), f64(w.scales), w.group)
+
+
+def _x(M, K, seed):
+    return torch.randn(M, K, generator=torch.Generator("cpu").manual_seed(seed)).to(BF)
+
+
+# group, K: one group (most warps idle), fewer groups than warps, more, an odd number of them
+WIDTHS = [(32, 32), (32, 320), (32, 1056), (64, 64), (64, 576), (64, 1088), (128, 128), (128, 1152), (128, 2176)]
+
+
+@pytest.mark.parametrize("group,K", WIDTHS)
+@pytest.mark.parametrize("M,N", [(1, 8), (1, 200), (2, 16), (5, 24), (8, 264), (9, 40), (16, 72), (17, 136), (33, 16),
+                                 (64, 104)])
+def test_linear(M, N, group, K):
+    w, x = _weight(N, K, group, seed=N + K), _x(M, K, seed=M)
+    buf = torch.full((M * N + 64,), -7.0, dtype=BF, device=DEV)
+    y = rglru.w4_linear(w, x.to(DEV), y=buf[32:32 + M * N].view(M, N))
+    assert (buf[:32] == -7).all() and (buf[32 + M * N:] == -7).all()
+    W = _dense(w)
+    ref = f64(x) @ W.T
+    _, bound = w4_bound(f64(x), W, ref)
+    err = np.abs(f64(y) - ref)
+    print(f"worst error / bound {np.max(err / bound):.3f}")
+    assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("group,K", WIDTHS[1::2])
+@pytest.mark.parametrize("M,H", [(1, 8), (3, 72), (8, 136), (12, 24), (40, 40)])
+def test_glu(M, H, group, K, act):
+    wg, wu, x = _weight(H, K, group, seed=K), _weight(H, K, group, seed=K + 1), _x(M, K, seed=M)
+    h = rglru.w4_glu(wg, wu, x.to(DEV), activation=act)
+    Wg, Wu = _dense(wg), _dense(wu)
+    g, u = f64(x) @ Wg.T, f64(x) @ Wu.T
+    eg, eu = w4_bound(f64(x), Wg, g)[0], w4_bound(f64(x), Wu, u)[0]
+    a = ff.act(g, act)
+    ea = 1.13 * eg + ACT * (np.abs(g) + eg)
+    e = ea * np.abs(u) + (np.abs(a) + ea) * eu
+    bound = (e + HALF * (np.abs(a * u) + e)) * (1 + 1e-6) + TINY
+    err = np.abs(f64(h) - a * u)
+    print(f"worst error / bound {np.max(err / bound):.3f}")
+    assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize(group):
+    """Codes and scales from their definition: the same IEEE float32 divisions."""
+    g = torch.Generator("cpu").manual_seed(group)
+    W = torch.randn(24, 3 * group, generator=g)
+    W[0, :group] = 0
+    W[1] *= 1e-37
+    W[2] *= 1e36
+    W[3, :group] = W[3, 0]
+    W = W.to(BF)
+    W[4, 1], W[5, group + 2] = float("inf"), float("nan")
+    q = rglru.w4_quantize(W.to(DEV), group)
+    v = W.float().view(24, 3, group)
+    s = (v.abs().amax(2) / 7).to(BF)
+    bad = ~torch.isfinite(v).all(2)
+    assert torch.isnan(q.scales.cpu()[bad]).all() and torch.equal(q.scales.cpu()[~bad], s[~bad])
+    c = torch.where((bad | (s == 0)).unsqueeze(2), torch.zeros_like(v),
+                    torch.round(v / s.float().unsqueeze(2)).clamp(-7, 7))
+    c = (c + 8).to(torch.uint8).view(24, -1, 2)
+    assert torch.equal(q.codes.cpu(), c[:, :, 0] | (c[:, :, 1] << 4))
+    # the weight is within half a step of its code, where nothing is out of the ordinary
+    ok = slice(6, 24)
+    dense = torch.from_numpy(_dense(q))[ok].view(18, 3, group)
+    assert ((dense - v[ok].double()).abs() <= s[ok].double().unsqueeze(2) * 0.5 * (1 + 2 ** -22)).all()
+
+
+def test_quantized_weight_serves_the_block():
+    """The operators together: a gated block's weights in 4 bits, its two linears and the projection down,
+    against the block on the weights those codes stand for."""
+    g = torch.Generator("cpu").manual_seed(1)
+    D, H, M = 256, 520, 4
+    Wg, Wu = ((torch.randn(H, D, generator=g) / D ** 0.5).to(BF).to(DEV) for _ in range(2))
+    x = _x(M, D, seed=2).to(DEV)
+    qg, qu = rglru.w4_quantize(Wg, 64), rglru.w4_quantize(Wu, 64)
+    h = rglru.w4_glu(qg, qu, x)
+    g_, u_ = rglru.w4_linear(qg, x), rglru.w4_linear(qu, x)
+    # the linears' outputs are rounded to bf16 before the product: 2^-8 each on g (slope ≤ 1.13, |g| ≤ …) and u
+    a = ff.act(f64(g_), "gelu")
+    ref = a * f64(u_)
+    tol = 1.13 * HALF * np.abs(f64(g_)) * np.abs(f64(u_)) * 1.02 + 2.05 * HALF * np.abs(ref) + 1e-5
+    assert (np.abs(f64(h) - ref) <= tol).all()
+
+
+def test_scales_and_non_finite_stay_where_they_are():
+    w, x = _weight(40, 256, 64, seed=3), _x(3, 256, seed=4).to(DEV)
+    clean = rglru.w4_linear(w, x)
+    s = w.scales.clone()
+    s[7, 1], s[39, 3] = float("nan"), float("inf")
+    y = rglru.w4_linear(rglru.W4Weight(w.codes, s, 64), x)
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[[7, 39]] = False
+    assert torch.equal(y[:, keep], clean[:, keep]) and not torch.isfinite(y[:, ~keep]).any()
+    bad = x.clone()
+    bad[1, 100] = float("nan")
+    y = rglru.w4_linear(w, bad)
+    assert torch.isnan(y[1]).all() and torch.equal(y[::2], clean[::2])
+
+
+def test_more_tokens_give_the_same_rows():
+    """A token's result does not depend on how many others are with it."""
+    w, x = _weight(72, 640, 128, seed=5), _x(64, 640, seed=6).to(DEV)
+    want = rglru.w4_linear(w, x)
+    for M in (1, 8, 9, 16, 20, 32, 50):
+        assert torch.equal(rglru.w4_linear(w, x[:M].contiguous()), want[:M]), M
+
+
+def test_streams_and_graphs():
+    w, x = _weight(72, 640, 128, seed=5), _x(6, 640, seed=6).to(DEV)
+    want = rglru.w4_linear(w, x), rglru.w4_glu(w, w, x)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(rglru.w4_linear(w, x, stream=s), rglru.w4_glu(w, w, x, stream=s)) for s in (a, b, a, b)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, want[0]) and torch.equal(q, want[1]) for p, q in got)
+    xin = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = rglru.w4_linear(w, xin), rglru.w4_glu(w, w, xin)
+    x2 = _x(6, 640, seed=8).to(DEV)
+    xin.copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, rglru.w4_linear(w, x2)) and torch.equal(h, rglru.w4_glu(w, w, x2))
+
+
+def test_binding_refusals():
+    w, x = _weight(16, 128, 64, seed=1), _x(2, 128, seed=1).to(DEV)
+    cases = [
+        (ValueError, lambda: rglru.w4_linear(w, x[:, :64].contiguous())),
+        (TypeError, lambda: rglru.w4_linear(w, x.float())),
+        (rglru._abi.RGLRUError, lambda: rglru.w4_linear(w, _x(65, 128, seed=1).to(DEV))),
+        (rglru._abi.RGLRUError, lambda: rglru.w4_linear(w, x[:0])),
+        (ValueError, lambda: rglru.w4_linear(rglru.W4Weight(w.codes, w.scales, 128), x)),
+        (ValueError, lambda: rglru.w4_linear(rglru.W4Weight(w.codes, w.scales, 16), x)),
+        (ValueError, lambda: rglru.w4_quantize(x, 256)),
+        (rglru._abi.RGLRUError, lambda: rglru.w4_quantize(x, 64)),  # two rows
+        (ValueError, lambda: rglru.w4_glu(w, _weight(24, 128, 64, seed=1), x)),
+    ]
+    for i, (err, call) in enumerate(cases):
+        with pytest.raises(err):
+            call()
+            raise AssertionError(f"case {i} was taken")
