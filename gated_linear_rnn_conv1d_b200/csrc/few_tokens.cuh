@@ -1,0 +1,423 @@
+// Products of a few tokens (M ≤ 64) with weight matrices: y = x Wᵀ, or the gated pair
+// h = act(x W_gᵀ) ⊙ (x W_uᵀ). What bounds them is the weights' way from HBM, each byte read once, so
+// the kernel is a stream of weights with the products on the side:
+//
+// * A block takes a tile of 16·MT weight rows; in the gated form 8 channels make 16 rows, the gate's
+//   in rows 0–7 and the up projection's in 8–15, so that a thread ends with g and u of the same
+//   channel and token. Its eight warps take the row's segments (SEG bytes of each row) in turn.
+// * Each warp copies its segments into a ring of its own in shared memory (cp.async), kRing segments deep
+//   and across tile borders: the bytes in flight that HBM's latency wants cost no registers and no
+//   barrier. An SM holds two blocks: 16 warps · (kRing − 1) · 16·MT·SEG bytes, up to 96 KB, in flight.
+//   (TMA boxes of 64 bytes by 16 or 32 rows in the place of these copies were slower: 50 µs against
+//   41 µs for 201 MB of bf16 weights.)
+// * The products run on mma.sync m16n8k16 with the weights as the row operand, eight tokens as the
+//   columns (the tcgen05 form would want x and unpacked weights in swizzled shared memory for work
+//   that is a few percent of the pipe). Lane 4r + t holds row r and r + 8 of the tile. Which k a slot
+//   of the MMA stands for is free as long as both operands agree: a lane's slots are neighbouring k.
+// * The eight warps' sums meet in shared memory, in a fixed order: results do not depend on the
+//   run, nor on how many tokens there are.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "act_math.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace rglru {
+
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * kFewWarps;
+
+struct FewArgs {
+  const uint8_t* w0;             // [rows] rows of row_bytes; the gate's in the gated form
+  const uint8_t* w1;             // the up projection's
+  const __nv_bfloat16* scales0;  // 4-bit weights: [rows][K / G]
+  const __nv_bfloat16* scales1;
+  const __nv_bfloat16* x;        // [M][K]
+  __nv_bfloat16* out;            // [M][rows]
+  int64_t row_bytes;             // a multiple of 16
+  int M, rows, K, granules;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool real) {
+  const int bytes = real ? 16 : 0;  // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where byte `byte` of row `row` of a segment lies in shared memory: its 16-byte pieces are permuted within
+// the row so that the lanes' reads (READ bytes each: a quad's lanes side by side, eight rows) meet no
+// bank twice.
+template <int SEG, int READ> __device__ __forceinline__ int seg_offset(int row, int byte) {
+  const int f = SEG == 128 ? (READ == 16 ? (row & 1) << 2 : READ == 8 ? (row & 3) << 1 : row & 7)
+                           : (READ == 16 ? 0 : READ == 8 ? (row & 2) : (row >> 1) & 3);
+  return row * SEG + (((byte / 16) ^ f) * 16) + byte % 16;
+}
+
+// A format's lane state: x rows of the lane's tokens (columns beyond M repeat the last token's; they are
+// not stored), and what is loaded a segment ahead of its use.
+
+// bf16 weights.
+struct FewBf16 {
+  static constexpr int kRead = 16;
+  template <int MT, int SEG, bool GLU> struct Ahead {  // nothing but the weights
+    __device__ void rows(const FewArgs&, int, int) {}
+    __device__ void load(const FewArgs&, int) {}
+  };
+  static __device__ __forceinline__ int lane_k(int t) { return 8 * t; }
+  // x of a segment, as eight-value pieces; the lane's piece c is 32·c further
+  template <int SEG> static constexpr int kX = SEG / 64;
+  template <int SEG> static __device__ __forceinline__ uint4 load_x(const FewArgs& a, const __nv_bfloat16* xrow,
+                                                                    int seg, int c, int lane) {
+    const int k = seg * (SEG / 2) + c * 32;  // beyond K the weights are zeros; x is made so too
+    return k + 8 * (lane % 4) < a.K ? __ldg(reinterpret_cast<const uint4*>(xrow + k)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  template <int NT, int MT, int SEG, class A>
+  static __device__ __forceinline__ void consume(const FewArgs& a, const uint8_t* seg_smem, int seg, int lane, int mt,
+                                                 const uint4 (&x)[NT][kX<SEG>], const A&, float (&acc)[MT][NT][4]) {
+    const int r = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int c = 0; c < SEG / 64; ++c) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (MT > 1 && m >= mt) break;
+        const uint4 wa = *reinterpret_cast<const uint4*>(seg_smem + seg_offset<SEG, 16>(16 * m + r, 64 * c + 16 * t));
+        const uint4 wb = *reinterpret_cast<const uint4*>(seg_smem + seg_offset<SEG, 16>(16 * m + 8 + r, 64 * c + 16 * t));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_bf16(acc[m][j], wa.x, wb.x, wa.y, wb.y, x[j][c].x, x[j][c].y);
+          mma_bf16(acc[m][j], wa.z, wb.z, wa.w, wb.w, x[j][c].z, x[j][c].w);
+        }
+      }
+    }
+  }
+};
+
+// 4-bit weights with a bf16 scale for each GROUP inputs of a row: Ŵ = s (q − 8). q − 8 is exact in bf16,
+// so a group's sum carries float32's rounding only, and its scale multiplies that sum in float32.
+template <int GROUP> struct FewW4 {
+  static constexpr int kWords = GROUP / 32;  // of a lane's quarter of a group
+  static constexpr int kRead = 4 * kWords;
+  // A segment's scales, loaded while the one before is worked on: lane l has those of the chunk's rows l and
+  // 32 + l, and hands them to the rows' quads by shuffles.
+  template <int MT, int SEG, bool GLU> struct Ahead {
+    static constexpr int kGroups = 2 * SEG / GROUP;
+    static constexpr int kHalves = (MT + 1) / 2;  // of the chunk, 32 rows each
+    const __nv_bfloat16* row[kHalves];
+    float s[kHalves][kGroups];
+    // granules from `first` on
+    __device__ __forceinline__ void rows(const FewArgs& a, int first, int lane) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const int l = 32 * h + lane % (MT == 1 ? 16 : 32), rr = l % 16;
+        const int n = min(GLU ? (first + l / 16) * 8 + rr % 8 : first * 16 + l, a.rows - 1);
+        row[h] = (GLU && rr >= 8 ? a.scales1 : a.scales0) + (int64_t)n * (a.K / GROUP);
+      }
+    }
+    __device__ __forceinline__ void load(const FewArgs& a, int seg) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int at = seg * kGroups + g;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) s[h][g] = at * GROUP < a.K ? __bfloat162float(__ldg(row[h] + at)) : 0.0f;
+      }
+    }
+  };
+  static __device__ __forceinline__ int lane_k(int t) { return 8 * kWords * t; }
+  // Four bf16 pairs (k, k + 4), k = 0 … 3, of a word's eight weights, less 8: 0x4300 is 128, and four
+  // bits in the mantissa's last places make 128 + q.
+  static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&p)[4]) {
+    const __nv_bfloat162 bias = __floats2bfloat162_rn(136.0f, 136.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t b;  // (w >> 4i) & 0x000F000F | 0x43004300 in one operation after the shift
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), bias);
+      p[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+  }
+  static __device__ __forceinline__ void read(const uint8_t* p, uint32_t (&w)[kWords]) {
+    if constexpr (kWords == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  // x of a segment: piece g·kWords + o is octet o of the lane's quarter of group g
+  template <int SEG> static constexpr int kX = 2 * SEG / GROUP * kWords;
+  template <int SEG> static __device__ __forceinline__ uint4 load_x(const FewArgs& a, const __nv_bfloat16* xrow,
+                                                                    int seg, int c, int) {
+    const int k = seg * (2 * SEG) + c / kWords * GROUP;
+    return k < a.K ? __ldg(reinterpret_cast<const uint4*>(xrow + k + 8 * (c % kWords))) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  template <int NT, int MT, int SEG, class A>
+  static __device__ __forceinline__ void consume(const FewArgs& a, const uint8_t* seg_smem, int seg, int lane, int mt,
+                                                 const uint4 (&x)[NT][kX<SEG>], const A& ahead,
+                                                 float (&acc)[MT][NT][4]) {
+    const int r = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int g = 0; g < 2 * SEG / GROUP; ++g) {
+      if (seg * (2 * SEG) + g * GROUP >= a.K) break;  // (the same for the whole warp)
+      const int byte = g * (GROUP / 2) + t * (4 * kWords);
+      uint32_t xp[kWords][NT][4];  // x in the unpacked weights' order
+#pragma unroll
+      for (int o = 0; o < kWords; ++o)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 v = x[j][g * kWords + o];
+          xp[o][j][0] = __byte_perm(v.x, v.z, 0x5410);
+          xp[o][j][1] = __byte_perm(v.x, v.z, 0x7632);
+          xp[o][j][2] = __byte_perm(v.y, v.w, 0x5410);
+          xp[o][j][3] = __byte_perm(v.y, v.w, 0x7632);
+        }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (MT > 1 && m >= mt) break;
+        uint32_t wa[kWords], wb[kWords];
+        read(seg_smem + seg_offset<SEG, kRead>(16 * m + r, byte), wa);
+        read(seg_smem + seg_offset<SEG, kRead>(16 * m + 8 + r, byte), wb);
+        float part[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) part[j][c] = 0.0f;
+#pragma unroll
+        for (int o = 0; o < kWords; ++o) {
+          uint32_t da[4], db[4];
+          unpack(wa[o], da);
+          unpack(wb[o], db);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_bf16(part[j], da[0], db[0], da[1], db[1], xp[o][j][0], xp[o][j][1]);
+            mma_bf16(part[j], da[2], db[2], da[3], db[3], xp[o][j][2], xp[o][j][3]);
+          }
+        }
+        const float fa = __shfl_sync(0xffffffffu, ahead.s[m / 2][g], 16 * (m % 2) + r);
+        const float fb = __shfl_sync(0xffffffffu, ahead.s[m / 2][g], 16 * (m % 2) + 8 + r);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[m][j][0] = fmaf(fa, part[j][0], acc[m][j][0]);
+          acc[m][j][1] = fmaf(fa, part[j][1], acc[m][j][1]);
+          acc[m][j][2] = fmaf(fb, part[j][2], acc[m][j][2]);
+          acc[m][j][3] = fmaf(fb, part[j][3], acc[m][j][3]);
+        }
+      }
+    }
+  }
+};
+
+// Shapes of the ring and of the sums: two sum buffers (one barrier a chunk) where they are small.
+template <int NT, int MT, int SEG, int RING> struct FewCfg {
+  static constexpr int kSegBytes = 16 * MT * SEG;
+  static constexpr int kRingBytes = kFewWarps * RING * kSegBytes;
+  static constexpr int kSumFloats = kFewWarps * MT * NT * 4 * 32;
+  static constexpr int kSumBufs = MT * NT <= 2 ? 2 : 1;
+  static constexpr int kSmem = kRingBytes + kSumBufs * kSumFloats * 4;
+  static constexpr int kBlocks = NT <= 2 ? 2 : 1;  // per SM
+  static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int RING>
+__global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, RING>::kBlocks) few_kernel(const FewArgs a) {
+  using Cfg = FewCfg<NT, MT, SEG, RING>;
+  constexpr int kGran = GLU ? 8 : 16;         // output columns of a granule: 16 weight rows
+  constexpr int kPieces = SEG / 16;           // of a row's segment
+  constexpr int kCopies = 16 * kPieces / 32;  // a lane's copies of a granule's segment
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint8_t* ring = few_smem + warp * RING * Cfg::kSegBytes;
+  float* sums = reinterpret_cast<float*>(few_smem + Cfg::kRingBytes);
+  const int segs = (int)((a.row_bytes + SEG - 1) / SEG);
+  const int my_segs = segs > warp ? (segs - warp + kFewWarps - 1) / kFewWarps : 0;
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // This block's granules [first, first + count), in chunks of at most MT
+  const int each = a.granules / (int)gridDim.x, more = a.granules % (int)gridDim.x;
+  const int count = each + ((int)blockIdx.x < more ? 1 : 0);
+  const int first = blockIdx.x * each + min((int)blockIdx.x, more);
+  const int chunks = (count + MT - 1) / MT;
+  auto chunk_at = [&](int c) { return first + c * count / chunks; };  // (count is small)
+
+  // The copies' place in the warp's sequence of segments, chunk by chunk. Copy i of a granule takes kStep
+  // rows, a lane the piece `piece` of one of them: a block of rows that belongs to one matrix, and that
+  // the last granule has whole or not at all (rows is a multiple of 8); rows it has not are computed from
+  // what is in shared memory and not stored.
+  constexpr int kStep = 32 / kPieces;
+  const int piece = lane % kPieces, lr = lane / kPieces;
+  int c_chunk = 0, c_left = my_segs, c_slot = 0, c_mt = 0, c_rows = 0;
+  int64_t c_byte = 0;  // of the row
+  const uint8_t *c_p0 = nullptr, *c_p1 = nullptr;
+  auto copy_chunk = [&] {
+    const int gr = chunk_at(c_chunk);
+    c_mt = chunk_at(c_chunk + 1) - gr;
+    c_rows = a.rows - gr * kGran;
+    const int64_t at = (int64_t)(gr * kGran + lr) * a.row_bytes;
+    c_byte = (int64_t)warp * SEG + piece * 16;
+    c_p0 = a.w0 + at;
+    if (GLU) c_p1 = a.w1 + at;
+    c_left = my_segs;
+  };
+  copy_chunk();
+  auto copy_next = [&] {
+    if (c_left > 0) {
+      const bool real = c_byte < a.row_bytes;
+      uint8_t* dst = ring + c_slot * Cfg::kSegBytes;
+      const int64_t byte = real ? c_byte : 0;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m < c_mt) {
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) {
+            const int row = i * kStep;
+            const int off = m * kGran + (GLU ? row % 8 : row);
+            const uint8_t* src = (GLU && row >= 8 ? c_p1 : c_p0) + off * a.row_bytes + byte;
+            if (off < c_rows)
+              cp_async_16(smem_u32(dst + seg_offset<SEG, F::kRead>(16 * m + row + lr, 16 * piece)), src, real);
+          }
+        }
+      }
+      c_byte += kFewWarps * SEG;
+      if (--c_left == 0 && ++c_chunk < chunks) copy_chunk();
+    }
+    cp_async_commit();  // (an empty group too: the waits count groups)
+    c_slot = c_slot + 1 == RING ? 0 : c_slot + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < RING - 1; ++i) copy_next();
+
+  const __nv_bfloat16* xrow[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    xrow[j] = a.x + (int64_t)min(8 * j + lane / 4, a.M - 1) * a.K + F::lane_k(lane % 4);
+  constexpr int kX = F::template kX<SEG>;
+  constexpr bool kEarly = NT == 1;  // x is loaded a segment ahead
+  typename F::template Ahead<MT, SEG, GLU> next;
+  uint4 x_next[NT][kX];
+  auto load_x = [&](uint4(&x)[NT][kX], int seg) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < kX; ++c) x[j][c] = F::template load_x<SEG>(a, xrow[j], seg, c, lane);
+  };
+  if (my_segs > 0) {
+    next.rows(a, chunk_at(0), lane);
+    next.load(a, warp);
+    if (kEarly) load_x(x_next, warp);
+  }
+  int slot = 0, buf = 0;
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int gr = chunk_at(chunk), mt = chunk_at(chunk + 1) - gr;
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
+    for (int i = 0; i < my_segs; ++i) {
+      cp_async_wait<RING - 2>();
+      __syncwarp();  // the other lanes' pieces too; and all have read the slot that is filled next
+      copy_next();
+      const int seg = warp + i * kFewWarps;
+      const bool last = i + 1 == my_segs;
+      const int seg_next = last ? warp : seg + kFewWarps;
+      const auto now = next;
+      uint4 x[NT][kX];
+      if (kEarly) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < kX; ++c) x[j][c] = x_next[j][c];
+        load_x(x_next, seg_next);
+      } else {
+        load_x(x, seg);
+      }
+      if (last) next.rows(a, gr + mt, lane);  // (past the last granule: the last rows)
+      next.load(a, seg_next);
+      F::template consume<NT, MT, SEG>(a, ring + slot * Cfg::kSegBytes, seg, lane, mt, x, now, acc);
+      slot = slot + 1 == RING ? 0 : slot + 1;
+    }
+    float* s = sums + buf * Cfg::kSumFloats;
+    if (Cfg::kSumBufs == 1 && chunk > 0) __syncthreads();  // the last chunk's sums have been read
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[((warp * MT + m) * NT * 4 + 4 * j + c) * 32 + lane] = acc[m][j][c];
+    // With two buffers: whoever reads this one does so before it comes to the next chunk's barrier,
+    // and it is written again after that.
+    __syncthreads();
+    // value (row, token) of a 16-row granule is element (token & 1) + 2·(row / 8) of token tile token / 8 of
+    // lane 4·(row & 7) + (token & 7) / 2
+    const int cols = mt * kGran;
+    for (int i = threadIdx.x; i < MT * kGran * 8 * NT; i += kFewThreads) {
+      const int col = i % (MT * kGran), token = i / (MT * kGran);
+      const int m = col / kGran, row = col % kGran;
+      if (token >= a.M || col >= cols || gr * kGran + col >= a.rows) continue;
+      const float* p = s + (m * NT * 4 + 4 * (token / 8) + (token & 1) + 2 * (row / 8)) * 32 + 4 * (row & 7) +
+                       (token & 7) / 2;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) v += p[w * MT * NT * 4 * 32];
+      if constexpr (GLU) {
+        float u = 0.0f, none;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) u += p[w * MT * NT * 4 * 32 + 64];
+        v = v * act_gate<ACT, false>(v, none) * u;
+      }
+      a.out[(int64_t)token * a.rows + gr * kGran + col] = __float2bfloat16_rn(v);
+    }
+    if (Cfg::kSumBufs == 2) buf ^= 1;
+  }
+  cp_async_wait<0>();
+}
+
+template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int RING>
+cudaError_t launch_few(FewArgs a, cudaStream_t s) {
+  using Cfg = FewCfg<NT, MT, SEG, RING>;
+  auto kern = few_kernel<F, GLU, ACT, NT, MT, SEG, RING>;
+  static bool attr_set[64] = {};  // idempotent: a race sets it twice
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  a.granules = (a.rows + (GLU ? 7 : 15)) / (GLU ? 8 : 16);
+  const int room = num_sms() * Cfg::kBlocks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.granules < room ? a.granules : room);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits (pdl_wait)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace rglru

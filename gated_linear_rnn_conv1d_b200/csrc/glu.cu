@@ -357,6 +357,7 @@ int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
 
 cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
                                int act, unsigned* status, cudaStream_t s) {
+  if (N <= kGluFewTokens) return launch_glu_few(W_gate, W_up, x, h, (int)N, D, H, act, s);
   CUtensorMap ma, mg, mu;
   if (!make_map_2d(&ma, x, D, N, (uint64_t)D * 2, BK, 128) || !make_map_2d(&mg, W_gate, D, H, (uint64_t)D * 2, BK, 128) ||
       !make_map_2d(&mu, W_up, D, H, (uint64_t)D * 2, BK, 128))

@@ -1,0 +1,34 @@
+// The gated feed-forward block's forward for a few tokens (serving): h = act(x W_gᵀ) ⊙ (x W_uᵀ) with
+// x [N][D], N ≤ 16, bf16 weights streamed once by few_tokens.cuh's kernel.
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "few_tokens.cuh"
+#include "kernels.cuh"
+
+namespace rglru {
+namespace {
+// Up to eight tokens chunks of one granule and a ring of four are as fast as any (35 µs for 201 MB;
+// wider chunks or deeper rings 36 to 47 µs: x is read through what shared memory leaves of the L1); with
+// sixteen, x weighs twice as much and is shared by the chunk's two granules (39 µs against 47 µs).
+template <int ACT> cudaError_t launch_act(const FewArgs& a, cudaStream_t s) {
+  return a.M <= 8 ? launch_few<FewBf16, true, ACT, 1, 1, 128, 4>(a, s)
+                  : launch_few<FewBf16, true, ACT, 2, 2, 128, 2>(a, s);
+}
+}  // namespace
+
+cudaError_t launch_glu_few(const void* W_gate, const void* W_up, const void* x, void* h, int N, int D, int H, int act,
+                           cudaStream_t s) {
+  FewArgs a{};
+  a.w0 = static_cast<const uint8_t*>(W_gate);
+  a.w1 = static_cast<const uint8_t*>(W_up);
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.out = static_cast<__nv_bfloat16*>(h);
+  a.row_bytes = (int64_t)D * 2;
+  a.M = N;
+  a.rows = H;
+  a.K = D;
+  return act == kActGelu ? launch_act<kActGelu>(a, s) : launch_act<kActSilu>(a, s);
+}
+
+}  // namespace rglru

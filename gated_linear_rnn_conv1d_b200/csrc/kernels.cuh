@@ -216,6 +216,10 @@ cudaError_t launch_backward(const BwdArgs& g, const BwdLayout& L, void* ws, cuda
 // kActSilu (act_math.cuh).
 cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
                                int act, unsigned* status, cudaStream_t s);
+// the same for N ≤ kGluFewTokens, by the kernel that streams the weights past a few tokens
+constexpr int kGluFewTokens = 16;
+cudaError_t launch_glu_few(const void* W_gate, const void* W_up, const void* x, void* h, int N, int D, int H, int act,
+                           cudaStream_t s);
 struct GluBwdArgs {
   const void* W_gate;  // [H][D]
   const void* W_up;

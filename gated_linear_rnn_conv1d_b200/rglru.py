@@ -614,66 +614,57 @@ def _width(name: str, *widths: int) -> None:
             raise ValueError(f"{name}: {n} channels, at most 65536 are taken")
 
 
-def _check(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device) -> torch.Tensor:
-    """Raises unless t is a contiguous CUDA tensor of that type and shape on `device`."""
+def _check(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device: int) -> torch.Tensor:
+    """Raises unless t is a contiguous tensor of that type and shape on that CUDA device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: librglru takes CUDA tensors only")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: librglru takes contiguous tensors only")
-    return t
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    raise ValueError(f"{name}: librglru takes contiguous tensors only")
 
 
-class _Call:
-    """The device and stream of one call: the input's device has to be the current one (its
-    kernels are launched there). With a stream given, outputs and workspaces are allocated for
-    that stream, and the caching allocator is told that it reads the inputs."""
-
-    __slots__ = ("device", "stream", "handle")
-
-    def __init__(self, x: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        if not x.is_cuda:
-            raise ValueError("librglru takes CUDA tensors only")
-        self.device = x.device
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {x.device}, which is not the current device")
-        self.stream = stream
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def out(self, name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype) -> torch.Tensor:
-        return self.empty(shape, dtype) if t is None else _check(name, t, dtype, shape, self.device)
-
-    def workspace(self, nbytes: int, ws: Optional[torch.Tensor]) -> torch.Tensor:
-        if ws is None:
-            return self.empty(max(nbytes, 256), torch.uint8)
-        _p(ws)
-        if ws.device != self.device:
-            raise ValueError(f"the workspace is on {ws.device}, not on {self.device}")
-        return _workspace(nbytes, self.device, ws)
-
-    def reads(self, *tensors: torch.Tensor) -> None:
-        if self.stream is not None:
-            for t in tensors:
-                t.record_stream(self.stream)
+# The current stream's handle without a Stream object around it (3 µs of a decode call's ten).
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _glu_weights(W_gate: torch.Tensor, W_up: torch.Tensor, device) -> Tuple[int, int]:
+def _device_of(x: torch.Tensor) -> int:
+    """The index of x's device, which has to be the current one: kernels are launched there."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("librglru takes CUDA tensors only")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, which is not the current device")
+    return dev
+
+
+def _new(x: torch.Tensor, shape, dtype: torch.dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Uninitialised memory on x's device; with a stream given, allocated for that stream."""
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
+
+
+def _reads(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
+    """Tells the caching allocator that a stream other than their own reads these tensors."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _glu_weights(W_gate: torch.Tensor, W_up: torch.Tensor, device: int) -> Tuple[int, int]:
     if W_gate.dim() != 2:
         raise ValueError("W_gate must be [H][D]")
-    _check("W_gate", W_gate, torch.bfloat16, W_gate.shape, device)
-    _check("W_up", W_up, torch.bfloat16, W_gate.shape, device)
-    H, D = W_gate.shape
+    shape = W_gate.shape
+    _check("W_gate", W_gate, torch.bfloat16, shape, device)
+    _check("W_up", W_up, torch.bfloat16, shape, device)
+    H, D = shape
     _width("W_gate", H, D)
     return H, D
 
@@ -683,14 +674,20 @@ def glu_forward(W_gate: torch.Tensor, W_up: torch.Tensor, x: torch.Tensor, *, ac
     """rglru_glu_forward: h = act(x W_gateᵀ) ⊙ (x W_upᵀ), x [..., D] → h [..., H], bf16; activation
     'gelu' (exact) or 'silu'."""
     lib = _abi.load()
-    call = _Call(x, stream)
-    H, D = _glu_weights(W_gate, W_up, call.device)
-    _check("x", x, torch.bfloat16, (*x.shape[:-1], D), call.device)
-    h = call.out("h", h, (*x.shape[:-1], H), torch.bfloat16)
-    _abi.check("rglru_glu_forward", lib.rglru_glu_forward(
-        W_gate.data_ptr(), W_up.data_ptr(), x.data_ptr(), h.data_ptr(), x.numel() // D if D else 0, D, H,
-        _act(activation), call.handle))
-    call.reads(W_gate, W_up, x)
+    dev = _device_of(x)
+    H, D = _glu_weights(W_gate, W_up, dev)
+    lead = x.shape[:-1]
+    _check("x", x, torch.bfloat16, (*lead, D), dev)
+    if h is None:
+        h = _new(x, (*lead, H), torch.bfloat16, stream)
+    else:
+        _check("h", h, torch.bfloat16, (*lead, H), dev)
+    code = lib.rglru_glu_forward(W_gate.data_ptr(), W_up.data_ptr(), x.data_ptr(), h.data_ptr(),
+                                 x.numel() // D if D else 0, D, H, _act(activation),
+                                 _current_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _abi.check("rglru_glu_forward", code)
+    _reads(stream, W_gate, W_up, x)
     return h
 
 
@@ -707,28 +704,34 @@ class Act8:
     def shape(self) -> torch.Size:
         return self.codes.shape
 
-    def check(self, device) -> None:
-        if self.codes.dim() < 1:
+    def check(self, device: int) -> int:
+        """Raises unless codes and scales fit each other; returns the number of channels."""
+        shape = self.codes.shape
+        if len(shape) < 1:
             raise ValueError("codes must have at least one dimension")
-        _check("codes", self.codes, torch.int8, self.codes.shape, device)
-        _check("scales", self.scales, torch.uint8, (*self.shape[:-1], -(-self.shape[-1] // 32)), device)
+        _check("codes", self.codes, torch.int8, shape, device)
+        _check("scales", self.scales, torch.uint8, (*shape[:-1], -(-shape[-1] // 32)), device)
+        _width("codes", shape[-1])
+        return shape[-1]
 
 
 def act8_pack(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None) -> Act8:
     """rglru_act8_pack: x [..., C] (bf16 or float32, C a multiple of 8) → its 8-bit checkpoint."""
     lib = _abi.load()
-    call = _Call(x, stream)
-    io = _io(x)
-    if x.dim() < 1:
+    dev = _device_of(x)
+    io, shape = _io(x), x.shape
+    if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
-    _check("x", x, x.dtype, x.shape, call.device)
-    C = x.shape[-1]
+    _check("x", x, x.dtype, shape, dev)
+    C = shape[-1]
     _width("x", C)
-    codes = call.empty(x.shape, torch.int8)
-    scales = call.empty((*x.shape[:-1], -(-C // 32)), torch.uint8)
-    _abi.check("rglru_act8_pack", lib.rglru_act8_pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                                                      x.numel() // C if C else 0, C, io, call.handle))
-    call.reads(x)
+    codes = _new(x, shape, torch.int8, stream)
+    scales = _new(x, (*shape[:-1], -(-C // 32)), torch.uint8, stream)
+    code = lib.rglru_act8_pack(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), x.numel() // C if C else 0, C, io,
+                               _current_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _abi.check("rglru_act8_pack", code)
+    _reads(stream, x)
     return Act8(codes, scales, x.dtype)
 
 
@@ -736,14 +739,17 @@ def act8_unpack(a: Act8, *, x: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_act8_unpack: the activation x̂ that a checkpoint holds, in the type it was packed from."""
     lib = _abi.load()
-    call = _Call(a.codes, stream)
-    a.check(call.device)
-    C = a.shape[-1]
-    _width("codes", C)
-    x = call.out("x", x, a.shape, a.dtype)
-    _abi.check("rglru_act8_unpack", lib.rglru_act8_unpack(a.codes.data_ptr(), a.scales.data_ptr(), x.data_ptr(),
-                                                          a.codes.numel() // C if C else 0, C, _io(x), call.handle))
-    call.reads(a.codes, a.scales)
+    dev = _device_of(a.codes)
+    C = a.check(dev)
+    if x is None:
+        x = _new(a.codes, a.codes.shape, a.dtype, stream)
+    else:
+        _check("x", x, a.dtype, a.codes.shape, dev)
+    code = lib.rglru_act8_unpack(a.codes.data_ptr(), a.scales.data_ptr(), x.data_ptr(), x.numel() // C if C else 0, C,
+                                 _io(x), _current_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _abi.check("rglru_act8_unpack", code)
+    _reads(stream, a.codes, a.scales)
     return x
 
 
@@ -759,32 +765,37 @@ def glu_backward(W_gate: torch.Tensor, W_up: torch.Tensor, x: Union[torch.Tensor
     [..., D], dW_gate and dW_up [H][D] and, with want_h, the forward's h [..., H] (else None), bf16."""
     lib = _abi.load()
     packed = isinstance(x, Act8)
-    call = _Call(x.codes if packed else x, stream)
-    H, D = _glu_weights(W_gate, W_up, call.device)
-    lead = x.shape[:-1]
+    dev = _device_of(x.codes if packed else x)
+    H, D = _glu_weights(W_gate, W_up, dev)
+    bf16, lead = torch.bfloat16, x.shape[:-1]
     if packed:
-        x.check(call.device)
-        if x.shape[-1] != D:
+        if x.check(dev) != D:
             raise ValueError(f"the checkpoint has {x.shape[-1]} channels, the weights take {D}")
     else:
-        _check("x", x, torch.bfloat16, (*lead, D), call.device)
-    _check("dh", dh, torch.bfloat16, (*lead, H), call.device)
+        _check("x", x, bf16, (*lead, D), dev)
+    _check("dh", dh, bf16, (*lead, H), dev)
     N = dh.numel() // H if H else 0
-    bf16 = torch.bfloat16
-    out = {"dx": call.empty((*lead, D), bf16), "dW_gate": call.empty((H, D), bf16),
-           "dW_up": call.empty((H, D), bf16), "h": call.empty((*lead, H), bf16) if want_h else None}
-    ws = call.workspace(lib.rglru_glu_backward_workspace_bytes(N, D, H, int(packed)), workspace)
+    out = {"dx": _new(dh, (*lead, D), bf16, stream), "dW_gate": _new(dh, (H, D), bf16, stream),
+           "dW_up": _new(dh, (H, D), bf16, stream), "h": _new(dh, (*lead, H), bf16, stream) if want_h else None}
+    nbytes = lib.rglru_glu_backward_workspace_bytes(N, D, H, packed)
+    if workspace is None:
+        ws = _new(dh, max(nbytes, 256), torch.uint8, stream)
+    else:
+        _p(workspace)
+        if workspace.get_device() != dev:
+            raise ValueError(f"the workspace is on {workspace.device}, not on cuda:{dev}")
+        ws = _workspace(nbytes, dh.device, workspace)
     tail = (dh.data_ptr(), out["dx"].data_ptr(), out["dW_gate"].data_ptr(), out["dW_up"].data_ptr(),
             out["h"].data_ptr() if want_h else None, N, D, H, _act(activation), ws.data_ptr(),
-            ws.numel() * ws.element_size(), call.handle)
+            ws.numel() * ws.element_size(), _current_stream(dev) if stream is None else stream.cuda_stream)
     if packed:
         _abi.check("rglru_glu_backward_act8", lib.rglru_glu_backward_act8(
             W_gate.data_ptr(), W_up.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(), *tail))
-        call.reads(W_gate, W_up, x.codes, x.scales, dh)
+        _reads(stream, W_gate, W_up, x.codes, x.scales, dh)
     else:
         _abi.check("rglru_glu_backward", lib.rglru_glu_backward(W_gate.data_ptr(), W_up.data_ptr(), x.data_ptr(),
                                                                 *tail))
-        call.reads(W_gate, W_up, x, dh)
+        _reads(stream, W_gate, W_up, x, dh)
     return out
 
 
@@ -800,29 +811,33 @@ class W4Weight:
     def shape(self) -> Tuple[int, int]:
         return self.codes.shape[0], 2 * self.codes.shape[1]
 
-    def check(self, name: str, device) -> None:
-        if self.codes.dim() != 2 or self.group not in (32, 64, 128):
+    def check(self, name: str, device: int) -> Tuple[int, int]:
+        """Raises unless codes and scales fit each other; returns (N, K)."""
+        shape = self.codes.shape
+        if len(shape) != 2 or self.group not in (32, 64, 128):
             raise ValueError(f"{name}: codes must be [N][K/2], the group 32, 64 or 128")
-        N, K = self.shape
-        _width(name, N, K)
-        _check(f"{name}.codes", self.codes, torch.uint8, self.codes.shape, device)
+        N, K = shape[0], 2 * shape[1]
+        _check(f"{name}.codes", self.codes, torch.uint8, shape, device)
         _check(f"{name}.scales", self.scales, torch.bfloat16, (N, K // self.group), device)
+        _width(name, N, K)
+        return N, K
 
 
 def w4_quantize(W: torch.Tensor, group: int = 128, *, stream: Optional[torch.cuda.Stream] = None) -> W4Weight:
     """rglru_w4_quantize: W [N][K] bf16 → codes and scales; group 32, 64 or 128, a divisor of K."""
     lib = _abi.load()
-    call = _Call(W, stream)
+    dev = _device_of(W)
     if W.dim() != 2 or group not in (32, 64, 128):
         raise ValueError("W must be [N][K], the group 32, 64 or 128")
     N, K = W.shape
+    _check("W", W, torch.bfloat16, W.shape, dev)
     _width("W", N, K)
-    _check("W", W, torch.bfloat16, W.shape, call.device)
-    codes = call.empty((N, K // 2), torch.uint8)
-    scales = call.empty((N, K // group), torch.bfloat16)
-    _abi.check("rglru_w4_quantize", lib.rglru_w4_quantize(W.data_ptr(), codes.data_ptr(), scales.data_ptr(), N, K,
-                                                          group, call.handle))
-    call.reads(W)
+    codes = _new(W, (N, K // 2), torch.uint8, stream)
+    scales = _new(W, (N, K // group), torch.bfloat16, stream)
+    _abi.check("rglru_w4_quantize", lib.rglru_w4_quantize(
+        W.data_ptr(), codes.data_ptr(), scales.data_ptr(), N, K, group,
+        _current_stream(dev) if stream is None else stream.cuda_stream))
+    _reads(stream, W)
     return W4Weight(codes, scales, group)
 
 
@@ -830,15 +845,20 @@ def w4_linear(w: W4Weight, x: torch.Tensor, *, y: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_w4_linear: y = x Ŵᵀ, x [..., K] bf16 of at most 64 rows → y [..., N] bf16."""
     lib = _abi.load()
-    call = _Call(x, stream)
-    w.check("w", call.device)
-    N, K = w.shape
-    _check("x", x, torch.bfloat16, (*x.shape[:-1], K), call.device)
-    y = call.out("y", y, (*x.shape[:-1], N), torch.bfloat16)
-    _abi.check("rglru_w4_linear", lib.rglru_w4_linear(
-        w.codes.data_ptr(), w.scales.data_ptr(), x.data_ptr(), y.data_ptr(), x.numel() // K if K else 0, N, K,
-        w.group, call.handle))
-    call.reads(w.codes, w.scales, x)
+    dev = _device_of(x)
+    N, K = w.check("w", dev)
+    lead = x.shape[:-1]
+    _check("x", x, torch.bfloat16, (*lead, K), dev)
+    if y is None:
+        y = _new(x, (*lead, N), torch.bfloat16, stream)
+    else:
+        _check("y", y, torch.bfloat16, (*lead, N), dev)
+    code = lib.rglru_w4_linear(w.codes.data_ptr(), w.scales.data_ptr(), x.data_ptr(), y.data_ptr(),
+                               x.numel() // K if K else 0, N, K, w.group,
+                               _current_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _abi.check("rglru_w4_linear", code)
+    _reads(stream, w.codes, w.scales, x)
     return y
 
 
@@ -846,18 +866,23 @@ def w4_glu(w_gate: W4Weight, w_up: W4Weight, x: torch.Tensor, *, activation: str
            h: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_w4_glu: h = act(x Ŵ_gateᵀ) ⊙ (x Ŵ_upᵀ), x [..., D] bf16 of at most 64 rows → h [..., H]."""
     lib = _abi.load()
-    call = _Call(x, stream)
-    w_gate.check("w_gate", call.device)
-    w_up.check("w_up", call.device)
-    if w_gate.shape != w_up.shape or w_gate.group != w_up.group:
+    dev = _device_of(x)
+    H, D = w_gate.check("w_gate", dev)
+    if w_up.check("w_up", dev) != (H, D) or w_gate.group != w_up.group:
         raise ValueError("w_gate and w_up differ in shape or group")
-    H, D = w_gate.shape
-    _check("x", x, torch.bfloat16, (*x.shape[:-1], D), call.device)
-    h = call.out("h", h, (*x.shape[:-1], H), torch.bfloat16)
-    _abi.check("rglru_w4_glu", lib.rglru_w4_glu(
-        w_gate.codes.data_ptr(), w_gate.scales.data_ptr(), w_up.codes.data_ptr(), w_up.scales.data_ptr(),
-        x.data_ptr(), h.data_ptr(), x.numel() // D if D else 0, H, D, w_gate.group, _act(activation), call.handle))
-    call.reads(w_gate.codes, w_gate.scales, w_up.codes, w_up.scales, x)
+    lead = x.shape[:-1]
+    _check("x", x, torch.bfloat16, (*lead, D), dev)
+    if h is None:
+        h = _new(x, (*lead, H), torch.bfloat16, stream)
+    else:
+        _check("h", h, torch.bfloat16, (*lead, H), dev)
+    code = lib.rglru_w4_glu(w_gate.codes.data_ptr(), w_gate.scales.data_ptr(), w_up.codes.data_ptr(),
+                            w_up.scales.data_ptr(), x.data_ptr(), h.data_ptr(), x.numel() // D if D else 0, H, D,
+                            w_gate.group, _act(activation),
+                            _current_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _abi.check("rglru_w4_glu", code)
+    _reads(stream, w_gate.codes, w_gate.scales, w_up.codes, w_up.scales, x)
     return h
 
 
