@@ -8,13 +8,13 @@
 //
 // One kernel shape: persistent CTA pairs (cta_group::2) on 256 × 256 output tiles, as the gate
 // GEMM's: warp 0 loads by TMA, warp 1 of the leader issues the MMAs, eight warps of each CTA
-// empty one accumulator while the next tile's MMAs fill the other. Four modes of it:
+// empty one accumulator while the next tile's MMAs fill the other. Three modes of it:
 //   GLU_FWD   h: rank 0 stages 128 rows of W_g, rank 1 the same 128 rows of W_u, so a tile holds
 //             g in columns 0–127 and u of the same channels in 128–255.
 //   GLU_GRAD  the same products; the epilogue reads dh and writes dg, du (and h when asked for).
-//   GLU_DX    dx: [dg | du]·[W_g; W_u], the weights read in place as an MN-major operand; k runs
-//             over dg's channels, then over du's.
-//   GLU_DW    dW_g and dW_u: dgᵀx and duᵀx, both operands MN-major in place, k over the tokens.
+//   GLU_WIDE  dx, dW_g and dW_u in one launch: [dg | du]·[W_g; W_u] with the weights read in place as
+//             an MN-major operand, k over dg's channels and then over du's; dgᵀx and duᵀx with both
+//             operands MN-major in place, k over the tokens.
 // Ragged sizes need no code in the loops: TMA fills what lies outside a matrix with zeros.
 #include <algorithm>
 #include <cstdint>
@@ -41,27 +41,64 @@ constexpr uint32_t kIdesc = umma_idesc_bf16_f32(256, 256);
 // a time then cover about 8 × 9 tiles, whose operands (17 · 256 rows of k) stay in L2 between them.
 constexpr int kBand = 8;
 
-enum GluMode { GLU_FWD = 0, GLU_GRAD = 1, GLU_DX = 2, GLU_DW = 3 };
+enum GluMode { GLU_FWD = 0, GLU_GRAD = 1, GLU_WIDE = 2 };
 
-struct GluGemmArgs {
-  int64_t M;           // output rows: N tokens, or H channels (GLU_DW)
-  int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
-  int tiles_m, tiles_n;
-  int tiles_half;      // GLU_DW: tile rows of dW_g (dW_u's follow)
-  int kb_half;         // GLU_DX: k-blocks of dg (du's follow)
+// One of the products of GLU_WIDE: a grid of 256 × 256 output tiles.
+struct GluProduct {
+  int64_t M;             // output rows
+  int tiles_m;
   int k_blocks;
-  __nv_bfloat16* out0;        // h | dg | dx | dW_g
-  __nv_bfloat16* out1;        // – | du | –  | dW_u
-  __nv_bfloat16* h;           // GLU_GRAD: h, or null
-  const __nv_bfloat16* dh;    // GLU_GRAD
+  __nv_bfloat16* out;
 };
 
-__device__ __forceinline__ void tile_of(const GluGemmArgs& a, int tile, int& m, int& n) {
-  const int band = tile / (kBand * a.tiles_n);
-  const int r = tile - band * kBand * a.tiles_n;
-  const int rows = min(kBand, a.tiles_m - band * kBand);
+struct GluGemmArgs {
+  int64_t M;           // GLU_FWD, GLU_GRAD: N tokens
+  int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
+  int tiles_m, tiles_n;
+  int k_blocks;
+  int wide;                   // rows of every matrix stored start on 32-byte borders
+  __nv_bfloat16* out0;        // h | dg
+  __nv_bfloat16* out1;        // – | du
+  __nv_bfloat16* h;           // GLU_GRAD: h, or null
+  const __nv_bfloat16* dh;    // GLU_GRAD
+  // GLU_WIDE: dx, dW_g and dW_u, whose tile columns all run over D; the products in the order in which
+  // their tiles are dealt out, the ones with the longest k first (the pairs then end together)
+  GluProduct p[3];
+  int dx;              // which of them is dx
+  int kb_half;         // dx: k-blocks of dg (du's follow)
+};
+
+struct Tile {
+  int m, n, k_blocks;
+  int which;  // GLU_WIDE: the product
+};
+__device__ __forceinline__ void tile_in(int tile, int tiles_m, int tiles_n, int& m, int& n) {
+  const int band = tile / (kBand * tiles_n);
+  const int r = tile - band * kBand * tiles_n;
+  const int rows = min(kBand, tiles_m - band * kBand);
   n = r / rows;
   m = band * kBand + r - n * rows;
+}
+template <int MODE> __device__ __forceinline__ Tile tile_of(const GluGemmArgs& a, int tile) {
+  Tile t{};
+  if constexpr (MODE != GLU_WIDE) {
+    tile_in(tile, a.tiles_m, a.tiles_n, t.m, t.n);
+    t.k_blocks = a.k_blocks;
+  } else {
+    int tiles_m = a.p[0].tiles_m;
+    t.k_blocks = a.p[0].k_blocks;
+#pragma unroll
+    for (int i = 1; i < 3; ++i) {
+      if (t.which == i - 1 && tile >= tiles_m * a.tiles_n) {
+        tile -= tiles_m * a.tiles_n;
+        tiles_m = a.p[i].tiles_m;
+        t.k_blocks = a.p[i].k_blocks;
+        t.which = i;
+      }
+    }
+    tile_in(tile, tiles_m, a.tiles_n, t.m, t.n);
+  }
+  return t;
 }
 
 __device__ __forceinline__ uint4 pack8(const float* f) {
@@ -69,13 +106,41 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// Sixteen columns of a row, from column `col` of `cols`: one 32-byte store where the rows allow it (a whole
+// sector of L2; two 16-byte stores are written as three), else one for each eight columns that exist.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16], int col, int cols, int wide) {
+  const uint4 a = pack8(v), b = pack8(v + 8);
+  if (wide && col + 16 <= cols) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    if (col < cols) *reinterpret_cast<uint4*>(p) = a;
+    if (col + 8 < cols) *reinterpret_cast<uint4*>(p + 8) = b;
+  }
+}
+
+// As mbar_wait, the thread asleep between its looks (the epilogue's and the loader's waits are long;
+// looking all the time costs issue slots and power).
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_sleep(a, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait_sleep(a, parity)) return true;
+    if (*abort || clock64() - t0 > kWaitCycles) return false;
+  }
+}
+
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                    const GluGemmArgs args, unsigned* status) {
-  constexpr bool kAMN = MODE == GLU_DW;                    // A MN-major
-  constexpr bool kBMN = MODE == GLU_DX || MODE == GLU_DW;  // B MN-major
+                    const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
+                    const __grid_constant__ CUtensorMap tmX, const GluGemmArgs args, int num_tiles, unsigned* status) {
+  // GLU_FWD, GLU_GRAD: A0 x, B0 W_g, B1 W_u. GLU_WIDE: A0 dg, A1 du, B0 W_g, B1 W_u (for dx); C0 dg, C1 du,
+  // X x (for dW, in boxes of 64 columns).
+  constexpr bool kGated = MODE != GLU_WIDE;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -92,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int cluster = blockIdx.x / 2;
   const int n_clusters = gridDim.x / 2;
-  const int num_tiles = args.tiles_m * args.tiles_n;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -110,8 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA0);
     tma_prefetch_desc(&tmB0);
-    if (MODE != GLU_DW) tma_prefetch_desc(&tmB1);
-    if (MODE == GLU_DX || MODE == GLU_DW) tma_prefetch_desc(&tmA1);
+    tma_prefetch_desc(&tmB1);
+    if (!kGated) {
+      tma_prefetch_desc(&tmA1);
+      tma_prefetch_desc(&tmC0);
+      tma_prefetch_desc(&tmC1);
+      tma_prefetch_desc(&tmX);
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
@@ -134,32 +203,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
-        int m, n;
-        tile_of(args, tile, m, n);
-        const bool second_m = MODE == GLU_DW && m >= args.tiles_half;
-        const int arow = (m - (second_m ? args.tiles_half : 0)) * 256 + (int)rank * 128;
-        const int bcol = MODE == GLU_FWD || MODE == GLU_GRAD ? n * 128 : n * 256 + (int)rank * 128;
-        for (int kb = 0; kb < args.k_blocks; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_s)) { ok = false; break; }
+        const Tile t = tile_of<MODE>(args, tile);
+        const int arow = t.m * 256 + (int)rank * 128;
+        const int bcol = kGated ? t.n * 128 : t.n * 256 + (int)rank * 128;
+        const bool is_dx = kGated || t.which == args.dx;
+        const bool second = !kGated && t.which > (args.dx == 0 ? 1 : 0);  // dW_u
+        for (int kb = 0; kb < t.k_blocks; ++kb) {
+          if (!wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s)) { ok = false; break; }
           uint8_t* sa = smem + stage * kStageBytes;
           uint8_t* sb = sa + kABytes;
           const uint32_t lbar = leader_full0 + stage * 8;
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStageBytes);
-          const bool second_k = MODE == GLU_DX && kb >= args.kb_half;
-          const int kc = (kb - (second_k ? args.kb_half : 0)) * BK;
-          const CUtensorMap* ma = second_m || second_k ? &tmA1 : &tmA0;
-          if constexpr (kAMN) {  // 128 columns as two boxes of 64 columns × BK rows
-            tma_load_2d_2sm(sa, ma, lbar, arow, kc);
-            tma_load_2d_2sm(sa + kABytes / 2, ma, lbar, arow + 64, kc);
+          if constexpr (kGated) {
+            tma_load_2d_2sm(sa, &tmA0, lbar, kb * BK, arow);
+            tma_load_2d_2sm(sb, leader ? &tmB0 : &tmB1, lbar, kb * BK, bcol);
           } else {
-            tma_load_2d_2sm(sa, ma, lbar, kc, arow);
-          }
-          if constexpr (kBMN) {
-            const CUtensorMap* mb = second_k ? &tmB1 : &tmB0;
+            // an MN-major operand: 128 columns as two boxes of 64 columns × BK rows
+            const bool du = kb >= args.kb_half;
+            const int kc = (is_dx && du ? kb - args.kb_half : kb) * BK;
+            const CUtensorMap* mb = is_dx ? (du ? &tmB1 : &tmB0) : &tmX;
+            if (is_dx) {
+              tma_load_2d_2sm(sa, du ? &tmA1 : &tmA0, lbar, kc, arow);
+            } else {
+              tma_load_2d_2sm(sa, second ? &tmC1 : &tmC0, lbar, arow, kc);
+              tma_load_2d_2sm(sa + kABytes / 2, second ? &tmC1 : &tmC0, lbar, arow + 64, kc);
+            }
             tma_load_2d_2sm(sb, mb, lbar, bcol, kc);
             tma_load_2d_2sm(sb + kBBytes / 2, mb, lbar, bcol + 64, kc);
-          } else {
-            tma_load_2d_2sm(sb, leader ? &tmB0 : &tmB1, lbar, kc, bcol);
           }
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
@@ -169,28 +239,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader CTA only) ----------------
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = kIdesc | (kAMN ? kIdescAMN : 0u) | (kBMN ? kIdescBMN : 0u);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
+        const Tile t = tile_of<MODE>(args, tile);
+        const bool a_mn = !kGated && t.which != args.dx;
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, &abort_s)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = 0; kb < args.k_blocks; ++kb) {
+        for (int kb = 0; kb < t.k_blocks; ++kb) {
           if (!mbar_wait(&full_bar[stage], phase, &abort_s)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + stage * kStageBytes);
           const uint32_t b_addr = a_addr + kABytes;
           // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box
+          const uint32_t first = kb == 0 ? 0u : 1u;
+          if (kGated) {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_f16_2sm(d_tmem,
-                         kAMN ? umma_desc_sw128_mn(a_addr + k * 2048, kABytes / 2) : umma_desc_sw128(a_addr + k * 32),
-                         kBMN ? umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2) : umma_desc_sw128(b_addr + k * 32),
-                         idesc, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < BK / 16; ++k)
+              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), kIdesc,
+                           k == 0 ? first : 1u);
+          } else if (a_mn) {
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              umma_f16_2sm(d_tmem, umma_desc_sw128_mn(a_addr + k * 2048, kABytes / 2),
+                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), kIdesc | kIdescAMN | kIdescBMN,
+                           k == 0 ? first : 1u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32),
+                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), kIdesc | kIdescBMN,
+                           k == 0 ? first : 1u);
+          }
           umma_commit_2sm_both(&empty_bar[stage]);
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
@@ -216,13 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = cluster; tile < num_tiles; tile += n_clusters) {
-      int m, n;
-      tile_of(args, tile, m, n);
-      const bool second_m = MODE == GLU_DW && m >= args.tiles_half;
-      const int64_t row = (int64_t)(m - (second_m ? args.tiles_half : 0)) * 256 + rank * 128 + quarter * 32 + lane;
-      const bool row_ok = row < args.M;
-      constexpr bool kGated = MODE == GLU_FWD || MODE == GLU_GRAD;
-      const int col0 = kGated ? n * 128 + half * 64 : n * 256 + half * 128;
+      const Tile t = tile_of<MODE>(args, tile);
+      int64_t rows = args.M;
+      __nv_bfloat16* out = args.out0;
+      if constexpr (!kGated) {
+        rows = t.which == 0 ? args.p[0].M : t.which == 1 ? args.p[1].M : args.p[2].M;
+        out = t.which == 0 ? args.p[0].out : t.which == 1 ? args.p[1].out : args.p[2].out;
+      }
+      const int64_t row = (int64_t)t.m * 256 + rank * 128 + quarter * 32 + lane;
+      const bool row_ok = row < rows;
+      const int col0 = kGated ? t.n * 128 + half * 64 : t.n * 256 + half * 128;
       const int64_t base = row * args.N + col0;
       // dh of this thread's row, loaded before the accumulator is ready
       [[maybe_unused]] uint4 dhq[MODE == GLU_GRAD ? 8 : 1];
@@ -232,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dhq[q] = row_ok && col0 + 8 * q < args.N ? __ldg(reinterpret_cast<const uint4*>(args.dh + base) + q)
                                                    : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (!mbar_wait(&tfull_bar[acc], acc_phase, &abort_s)) {
+      if (!wait_asleep(&tfull_bar[acc], acc_phase, &abort_s)) {
         abort_s = 1;
         atomicOr(status, kStatusTimeout);
         break;
@@ -253,49 +340,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x16(ta + (k + 1) * kStep, ra[cur ^ 1]);
           tmem_ld_x16(tb + (k + 1) * kStep, rb[cur ^ 1]);
         }
+        const int col = col0 + k * kStep;
+        const int64_t at = base + k * kStep;
+        float o0[16], o1[16];
+        if constexpr (kGated) {
+          [[maybe_unused]] float o2[16];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // eight columns of each, all inside the matrix or all outside
-          const int c = col0 + k * kStep + q * 8;
-          if constexpr (kGated) {
-            float o0[8];
-            [[maybe_unused]] float o1[8], o2[8];
+          for (int j = 0; j < 16; j += 2) {
+            const float2 g = make_float2(__uint_as_float(ra[cur][j]), __uint_as_float(ra[cur][j + 1]));
+            const float2 u = make_float2(__uint_as_float(rb[cur][j]), __uint_as_float(rb[cur][j + 1]));
+            float2 slope;
+            const float2 a = __fmul2_rn(g, act_gate2<ACT, MODE == GLU_GRAD>(g, slope));
+            const float2 hv = __fmul2_rn(a, u);
+            if constexpr (MODE == GLU_FWD) {
+              o0[j] = hv.x;
+              o0[j + 1] = hv.y;
+            } else {
+              const uint4 d4 = dhq[2 * k + j / 8];
+              const uint32_t w = j % 8 == 0 ? d4.x : j % 8 == 2 ? d4.y : j % 8 == 4 ? d4.z : d4.w;
+              const float2 d = make_float2(bf16lo(w), bf16hi(w));
+              // dg and du are rounded to bf16, the operands of the next products: half a step of 2^-8
+              // each, as much as the rounding of dx and dW themselves
+              const float2 dg = __fmul2_rn(__fmul2_rn(d, u), slope), du = __fmul2_rn(d, a);
+              o0[j] = dg.x;
+              o0[j + 1] = dg.y;
+              o1[j] = du.x;
+              o1[j + 1] = du.y;
+              o2[j] = hv.x;
+              o2[j + 1] = hv.y;
+            }
+          }
+          if (row_ok) {
+            store16(out + at, o0, col, args.N, args.wide);
+            if constexpr (MODE == GLU_GRAD) {
+              store16(args.out1 + at, o1, col, args.N, args.wide);
+              if (args.h != nullptr) store16(args.h + at, o2, col, args.N, args.wide);
+            }
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float g = __uint_as_float(ra[cur][q * 8 + j]), u = __uint_as_float(rb[cur][q * 8 + j]);
-              float slope = 0.0f;
-              const float a = g * act_gate<ACT, MODE == GLU_GRAD>(g, slope);
-              if constexpr (MODE == GLU_FWD) {
-                o0[j] = a * u;
-              } else {
-                const uint4 d4 = dhq[2 * k + q];
-                const uint32_t w = j < 2 ? d4.x : j < 4 ? d4.y : j < 6 ? d4.z : d4.w;
-                const float d = j % 2 == 0 ? bf16lo(w) : bf16hi(w);
-                // dg and du are rounded to bf16, the operands of the next products: half a step
-                // of 2^-8 each, as much as the rounding of dx and dW themselves
-                o0[j] = d * u * slope;
-                o1[j] = d * a;
-                o2[j] = a * u;
-              }
-            }
-            if (row_ok && c < args.N) {
-              const int64_t at = base + k * kStep + q * 8;
-              *reinterpret_cast<uint4*>(args.out0 + at) = pack8(o0);
-              if constexpr (MODE == GLU_GRAD) {
-                *reinterpret_cast<uint4*>(args.out1 + at) = pack8(o1);
-                if (args.h != nullptr) *reinterpret_cast<uint4*>(args.h + at) = pack8(o2);
-              }
-            }
-          } else {
-            __nv_bfloat16* out = second_m ? args.out1 : args.out0;
-            float v[8], w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              v[j] = __uint_as_float(ra[cur][q * 8 + j]);
-              w[j] = __uint_as_float(rb[cur][q * 8 + j]);
-            }
-            const int64_t at = base + k * kStep + q * 8;
-            if (row_ok && c < args.N) *reinterpret_cast<uint4*>(out + at) = pack8(v);
-            if (row_ok && c + 16 < args.N) *reinterpret_cast<uint4*>(out + at + 16) = pack8(w);
+          for (int j = 0; j < 16; ++j) {
+            o0[j] = __uint_as_float(ra[cur][j]);
+            o1[j] = __uint_as_float(rb[cur][j]);
+          }
+          if (row_ok) {
+            store16(out + at, o0, col, args.N, args.wide);
+            store16(out + at + 16, o1, col + 16, args.N, args.wide);
           }
         }
         if (k + 1 < 4) tmem_ld_wait16(ra[cur ^ 1], rb[cur ^ 1]);
@@ -317,9 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+struct Maps {
+  CUtensorMap a0, a1, b0, b1, c0, c1, x;
+};
+
 template <int MODE, int ACT>
-cudaError_t launch_mode(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
-                        const GluGemmArgs& args, unsigned* status, cudaStream_t s) {
+cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int64_t tiles, unsigned* status, cudaStream_t s) {
   auto kern = glu_gemm_kernel<MODE, ACT>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
@@ -331,7 +424,6 @@ cudaError_t launch_mode(const CUtensorMap& a0, const CUtensorMap& a1, const CUte
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int64_t tiles = (int64_t)args.tiles_m * args.tiles_n;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
   const int clusters = (int)std::min<int64_t>(tiles, num_sms() / 2);
   cudaLaunchConfig_t cfg = {};
@@ -348,81 +440,81 @@ cudaError_t launch_mode(const CUtensorMap& a0, const CUtensorMap& a1, const CUte
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a0, a1, b0, b1, args, status);
+  return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, args, (int)tiles, status);
 }
 
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
+bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// g and u of N tokens: the tensor maps and the tile grid of GLU_FWD and GLU_GRAD.
+bool gated_args(const void* W_gate, const void* W_up, const void* x, int64_t N, int D, int H, Maps& m,
+                GluGemmArgs& a) {
+  const uint64_t row = (uint64_t)D * 2;
+  if (!make_map_2d(&m.a0, x, D, N, row, BK, 128) || !make_map_2d(&m.b0, W_gate, D, H, row, BK, 128) ||
+      !make_map_2d(&m.b1, W_up, D, H, row, BK, 128))
+    return false;
+  m.a1 = m.c0 = m.c1 = m.x = m.a0;  // (not read)
+  a = GluGemmArgs{};
+  a.M = N;
+  a.N = H;
+  a.tiles_m = tiles_of(N, 256);
+  a.tiles_n = tiles_of(H, 128);
+  a.k_blocks = tiles_of(D, BK);
+  return true;
+}
 
 }  // namespace
 
 cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
                                int act, unsigned* status, cudaStream_t s) {
   if (N <= kGluFewTokens) return launch_glu_few(W_gate, W_up, x, h, (int)N, D, H, act, s);
-  CUtensorMap ma, mg, mu;
-  if (!make_map_2d(&ma, x, D, N, (uint64_t)D * 2, BK, 128) || !make_map_2d(&mg, W_gate, D, H, (uint64_t)D * 2, BK, 128) ||
-      !make_map_2d(&mu, W_up, D, H, (uint64_t)D * 2, BK, 128))
-    return cudaErrorInvalidValue;
-  GluGemmArgs a{};
-  a.M = N;
-  a.N = H;
-  a.tiles_m = tiles_of(N, 256);
-  a.tiles_n = tiles_of(H, 128);
-  a.k_blocks = tiles_of(D, BK);
+  Maps m;
+  GluGemmArgs a;
+  if (!gated_args(W_gate, W_up, x, N, D, H, m, a)) return cudaErrorInvalidValue;
   a.out0 = static_cast<__nv_bfloat16*>(h);
-  return act == kActGelu ? launch_mode<GLU_FWD, kActGelu>(ma, ma, mg, mu, a, status, s)
-                         : launch_mode<GLU_FWD, kActSilu>(ma, ma, mg, mu, a, status, s);
+  a.wide = H % 16 == 0 && on32(h);
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  return act == kActGelu ? launch_mode<GLU_FWD, kActGelu>(m, a, tiles, status, s)
+                         : launch_mode<GLU_FWD, kActSilu>(m, a, tiles, status, s);
 }
 
 cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStream_t s) {
   const int64_t N = b.N;
   const int D = b.D, H = b.H;
-  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)H * 2;
-  CUtensorMap a0, a1, b0, b1;
   // dg, du (and h) from x, the weights and dh
-  if (!make_map_2d(&a0, b.x, D, N, rowD, BK, 128) || !make_map_2d(&b0, b.W_gate, D, H, rowD, BK, 128) ||
-      !make_map_2d(&b1, b.W_up, D, H, rowD, BK, 128))
-    return cudaErrorInvalidValue;
-  GluGemmArgs g{};
-  g.M = N;
-  g.N = H;
-  g.tiles_m = tiles_of(N, 256);
-  g.tiles_n = tiles_of(H, 128);
-  g.k_blocks = tiles_of(D, BK);
-  g.out0 = static_cast<__nv_bfloat16*>(b.dg);
-  g.out1 = static_cast<__nv_bfloat16*>(b.du);
-  g.h = static_cast<__nv_bfloat16*>(b.h);
-  g.dh = static_cast<const __nv_bfloat16*>(b.dh);
-  cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(a0, a0, b0, b1, g, status, s)
-                                    : launch_mode<GLU_GRAD, kActSilu>(a0, a0, b0, b1, g, status, s);
+  Maps m;
+  GluGemmArgs a;
+  if (!gated_args(b.W_gate, b.W_up, b.x, N, D, H, m, a)) return cudaErrorInvalidValue;
+  a.out0 = static_cast<__nv_bfloat16*>(b.dg);
+  a.out1 = static_cast<__nv_bfloat16*>(b.du);
+  a.h = static_cast<__nv_bfloat16*>(b.h);
+  a.dh = static_cast<const __nv_bfloat16*>(b.dh);
+  a.wide = H % 16 == 0 && on32(b.dg) && on32(b.du) && on32(b.h);
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, tiles, status, s)
+                                    : launch_mode<GLU_GRAD, kActSilu>(m, a, tiles, status, s);
   if (e != cudaSuccess) return e;
-  // dx = dg W_g + du W_u
-  if (!make_map_2d(&a0, b.dg, H, N, rowH, BK, 128) || !make_map_2d(&a1, b.du, H, N, rowH, BK, 128) ||
-      !make_map_2d(&b0, b.W_gate, D, H, rowD, 64, BK) || !make_map_2d(&b1, b.W_up, D, H, rowD, 64, BK))
+  // dx = dg W_g + du W_u, dW_g = dgᵀ x, dW_u = duᵀ x
+  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)H * 2;
+  if (!make_map_2d(&m.a0, b.dg, H, N, rowH, BK, 128) || !make_map_2d(&m.a1, b.du, H, N, rowH, BK, 128) ||
+      !make_map_2d(&m.b0, b.W_gate, D, H, rowD, 64, BK) || !make_map_2d(&m.b1, b.W_up, D, H, rowD, 64, BK) ||
+      !make_map_2d(&m.c0, b.dg, H, N, rowH, 64, BK) || !make_map_2d(&m.c1, b.du, H, N, rowH, 64, BK) ||
+      !make_map_2d(&m.x, b.x, D, N, rowD, 64, BK))
     return cudaErrorInvalidValue;
-  GluGemmArgs dx{};
-  dx.M = N;
-  dx.N = D;
-  dx.tiles_m = tiles_of(N, 256);
-  dx.tiles_n = tiles_of(D, 256);
-  dx.kb_half = tiles_of(H, BK);
-  dx.k_blocks = 2 * dx.kb_half;
-  dx.out0 = static_cast<__nv_bfloat16*>(b.dx);
-  e = launch_mode<GLU_DX, kActGelu>(a0, a1, b0, b1, dx, status, s);
-  if (e != cudaSuccess) return e;
-  // dW_g = dgᵀ x, dW_u = duᵀ x
-  if (!make_map_2d(&a0, b.dg, H, N, rowH, 64, BK) || !make_map_2d(&a1, b.du, H, N, rowH, 64, BK) ||
-      !make_map_2d(&b0, b.x, D, N, rowD, 64, BK))
-    return cudaErrorInvalidValue;
-  GluGemmArgs dw{};
-  dw.M = H;
-  dw.N = D;
-  dw.tiles_half = tiles_of(H, 256);
-  dw.tiles_m = 2 * dw.tiles_half;
-  dw.tiles_n = tiles_of(D, 256);
-  dw.k_blocks = tiles_of(N, BK);
-  dw.out0 = static_cast<__nv_bfloat16*>(b.dW_gate);
-  dw.out1 = static_cast<__nv_bfloat16*>(b.dW_up);
-  return launch_mode<GLU_DW, kActGelu>(a0, a1, b0, b0, dw, status, s);
+  GluGemmArgs w{};
+  w.N = D;
+  w.tiles_n = tiles_of(D, 256);
+  w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);
+  w.kb_half = tiles_of(H, BK);
+  const GluProduct dx{N, tiles_of(N, 256), 2 * w.kb_half, static_cast<__nv_bfloat16*>(b.dx)};
+  const GluProduct dwg{H, tiles_of(H, 256), tiles_of(N, BK), static_cast<__nv_bfloat16*>(b.dW_gate)};
+  GluProduct dwu = dwg;
+  dwu.out = static_cast<__nv_bfloat16*>(b.dW_up);
+  w.dx = dx.k_blocks >= dwg.k_blocks ? 0 : 2;
+  w.p[w.dx] = dx;
+  w.p[w.dx == 0 ? 1 : 0] = dwg;
+  w.p[w.dx == 0 ? 2 : 1] = dwu;
+  return launch_mode<GLU_WIDE, kActGelu>(m, w, (int64_t)(dx.tiles_m + 2 * dwg.tiles_m) * w.tiles_n, status, s);
 }
 
 }  // namespace rglru
