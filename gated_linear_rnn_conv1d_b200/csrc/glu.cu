@@ -6,7 +6,7 @@
 // Five products of 2·N·D·H operations or six halves of them: the tensor cores bound every part,
 // so the elementwise work rides in the products' epilogues and g, u are never stored.
 //
-// One kernel shape: persistent CTA pairs (cta_group::2) on 256 × 256 output tiles, as the gate
+// One kernel shape: persistent CTA pairs (cta_group::2) on output tiles of up to 256 × 256, as the gate
 // GEMM's: warp 0 loads by TMA, warp 1 of the leader issues the MMAs, eight warps of each CTA
 // empty one accumulator while the next tile's MMAs fill the other. Three modes of it:
 //   GLU_FWD   h: rank 0 stages 128 rows of W_g, rank 1 the same 128 rows of W_u, so a tile holds
@@ -36,69 +36,75 @@ constexpr int kSmem = kStages * kStageBytes + 1024;
 constexpr int kTmemCols = 512;  // two 256-column accumulators
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kIdesc = umma_idesc_bf16_f32(256, 256);
 // Output tiles are taken in bands of kBand tile rows, column by column: the 74 pairs at work at
 // a time then cover about 8 × 9 tiles, whose operands (17 · 256 rows of k) stay in L2 between them.
 constexpr int kBand = 8;
 
 enum GluMode { GLU_FWD = 0, GLU_GRAD = 1, GLU_WIDE = 2 };
 
-// One of the products of GLU_WIDE: a grid of 256 × 256 output tiles.
+// A product's output: tiles_m × tiles_n tiles of 2·half_rows rows (each CTA's half, up to 128; where there
+// are few tokens, no more than they need: the MMA's other rows are made of what shared memory holds
+// and not stored) and `width` columns.
 struct GluProduct {
   int64_t M;             // output rows
-  int tiles_m;
+  int tiles_m, half_rows;
   int k_blocks;
   __nv_bfloat16* out;
 };
 
 struct GluGemmArgs {
-  int64_t M;           // GLU_FWD, GLU_GRAD: N tokens
   int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
-  int tiles_m, tiles_n;
-  int k_blocks;
-  int wide;                   // rows of every matrix stored start on 32-byte borders
-  __nv_bfloat16* out0;        // h | dg
-  __nv_bfloat16* out1;        // – | du
+  int tiles_n, width;  // of every product; width: channels (up to 128), or columns (up to 256)
+  int wide;            // rows of every matrix stored start on 32-byte borders
+  __nv_bfloat16* du;          // GLU_GRAD
   __nv_bfloat16* h;           // GLU_GRAD: h, or null
   const __nv_bfloat16* dh;    // GLU_GRAD
-  // GLU_WIDE: dx, dW_g and dW_u, whose tile columns all run over D; the products in the order in which
-  // their tiles are dealt out, the ones with the longest k first (the pairs then end together)
-  GluProduct p[3];
-  int dx;              // which of them is dx
   int kb_half;         // dx: k-blocks of dg (du's follow)
+  // p[0]: h or dg; or dx. p[1], p[2]: dW_g and dW_u, whose tiles are numbered through.
+  GluProduct p[3];
+  // How the tiles are dealt out. First the tiles with the longer k (dx's, or with dw_first dW's), one to
+  // each pair in turn; the pairs that the last turn leaves out (all but the first `rest`) take
+  // `extra` short ones in their place; the other short ones go round again, those pairs first.
+  int dw_first, n_long, n_short, rest, extra;
 };
 
 struct Tile {
-  int m, n, k_blocks;
-  int which;  // GLU_WIDE: the product
+  int m, n, which, k_blocks;
 };
-__device__ __forceinline__ void tile_in(int tile, int tiles_m, int tiles_n, int& m, int& n) {
-  const int band = tile / (kBand * tiles_n);
-  const int r = tile - band * kBand * tiles_n;
-  const int rows = min(kBand, tiles_m - band * kBand);
-  n = r / rows;
-  m = band * kBand + r - n * rows;
-}
-template <int MODE> __device__ __forceinline__ Tile tile_of(const GluGemmArgs& a, int tile) {
-  Tile t{};
-  if constexpr (MODE != GLU_WIDE) {
-    tile_in(tile, a.tiles_m, a.tiles_n, t.m, t.n);
-    t.k_blocks = a.k_blocks;
-  } else {
-    int tiles_m = a.p[0].tiles_m;
-    t.k_blocks = a.p[0].k_blocks;
-#pragma unroll
-    for (int i = 1; i < 3; ++i) {
-      if (t.which == i - 1 && tile >= tiles_m * a.tiles_n) {
-        tile -= tiles_m * a.tiles_n;
-        tiles_m = a.p[i].tiles_m;
-        t.k_blocks = a.p[i].k_blocks;
-        t.which = i;
-      }
+// The it-th tile of a pair; false when it has no more.
+template <int MODE>
+__device__ __forceinline__ bool tile_of(const GluGemmArgs& a, int it, int pair, int pairs, Tile& t) {
+  int64_t at = (int64_t)it * pairs + pair;
+  bool is_long = true;
+  if (at >= a.n_long) {
+    if (MODE != GLU_WIDE) return false;
+    is_long = false;
+    const bool late = pair >= a.rest;  // left out of the last turn
+    int i = it - (a.n_long - pair + pairs - 1) / pairs;
+    const int others = pairs - a.rest;
+    if (late && i < a.extra) {
+      at = (int64_t)i * others + pair - a.rest;
+    } else {
+      if (late) i -= a.extra;
+      at = (int64_t)a.extra * others + (int64_t)i * pairs + (late ? pair - a.rest : pair + others);
     }
-    tile_in(tile, tiles_m, a.tiles_n, t.m, t.n);
+    if (at >= a.n_short) return false;
   }
-  return t;
+  int tile = (int)at;
+  t.which = 0;
+  if (MODE == GLU_WIDE && is_long == (a.dw_first != 0)) {  // a tile of dW
+    const int each = a.p[1].tiles_m * a.tiles_n;
+    t.which = tile < each ? 1 : 2;
+    tile -= tile < each ? 0 : each;
+  }
+  const int tiles_m = t.which == 0 ? a.p[0].tiles_m : a.p[1].tiles_m;
+  t.k_blocks = t.which == 0 ? a.p[0].k_blocks : a.p[1].k_blocks;
+  const int band = tile / (kBand * a.tiles_n);
+  const int r = tile - band * kBand * a.tiles_n;
+  const int rows = min(kBand, tiles_m - band * kBand);
+  t.n = r / rows;
+  t.m = band * kBand + r - t.n * rows;
+  return true;
 }
 
 __device__ __forceinline__ uint4 pack8(const float* f) {
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                     const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-                    const __grid_constant__ CUtensorMap tmX, const GluGemmArgs args, int num_tiles, unsigned* status) {
+                    const __grid_constant__ CUtensorMap tmX, const GluGemmArgs args, unsigned* status) {
   // GLU_FWD, GLU_GRAD: A0 x, B0 W_g, B1 W_u. GLU_WIDE: A0 dg, A1 du, B0 W_g, B1 W_u (for dx); C0 dg, C1 du,
   // X x (for dW, in boxes of 64 columns).
   constexpr bool kGated = MODE != GLU_WIDE;
@@ -202,18 +208,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
-        const Tile t = tile_of<MODE>(args, tile);
-        const int arow = t.m * 256 + (int)rank * 128;
-        const int bcol = kGated ? t.n * 128 : t.n * 256 + (int)rank * 128;
-        const bool is_dx = kGated || t.which == args.dx;
-        const bool second = !kGated && t.which > (args.dx == 0 ? 1 : 0);  // dW_u
+      // this CTA's half of the tile's columns: `width` weight rows, or in one or two boxes of 64 columns
+      const int half_cols = kGated ? args.width : args.width / 2;
+      const bool two = !kGated && half_cols > 64;
+      const uint32_t b_bytes = kGated ? half_cols * BK * 2 : two ? kBBytes : kBBytes / 2;
+      Tile t;
+      for (int it = 0; ok && tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
+        const int half_rows = t.which == 0 ? args.p[0].half_rows : 128;
+        const int arow = (2 * t.m + (int)rank) * half_rows;
+        const uint32_t bytes = 2 * (half_rows * BK * 2 + b_bytes);
+        const int bcol = kGated ? t.n * args.width : t.n * args.width + (int)rank * half_cols;
+        const bool is_dx = kGated || t.which == 0;
+        const bool second = !kGated && t.which == 2;
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           if (!wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s)) { ok = false; break; }
           uint8_t* sa = smem + stage * kStageBytes;
           uint8_t* sb = sa + kABytes;
           const uint32_t lbar = leader_full0 + stage * 8;
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kStageBytes);
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
           if constexpr (kGated) {
             tma_load_2d_2sm(sa, &tmA0, lbar, kb * BK, arow);
             tma_load_2d_2sm(sb, leader ? &tmB0 : &tmB1, lbar, kb * BK, bcol);
@@ -229,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d_2sm(sa + kABytes / 2, second ? &tmC1 : &tmC0, lbar, arow + 64, kc);
             }
             tma_load_2d_2sm(sb, mb, lbar, bcol, kc);
-            tma_load_2d_2sm(sb + kBBytes / 2, mb, lbar, bcol + 64, kc);
+            if (two) tma_load_2d_2sm(sb + kBBytes / 2, mb, lbar, bcol + 64, kc);
           }
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
@@ -244,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int tile = cluster; tile < num_tiles && ok; tile += n_clusters) {
-        const Tile t = tile_of<MODE>(args, tile);
-        const bool a_mn = !kGated && t.which != args.dx;
+      const uint32_t idesc = umma_idesc_bf16_f32(256, kGated ? 2 * args.width : args.width);
+      Tile t;
+      for (int it = 0; ok && tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
+        const bool a_mn = !kGated && t.which != 0;
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, &abort_s)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
@@ -260,19 +273,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kGated) {
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
-              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), kIdesc,
+              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
                            k == 0 ? first : 1u);
           } else if (a_mn) {
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
               umma_f16_2sm(d_tmem, umma_desc_sw128_mn(a_addr + k * 2048, kABytes / 2),
-                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), kIdesc | kIdescAMN | kIdescBMN,
+                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), idesc | kIdescAMN | kIdescBMN,
                            k == 0 ? first : 1u);
           } else {
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
               umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32),
-                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), kIdesc | kIdescBMN,
+                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), idesc | kIdescBMN,
                            k == 0 ? first : 1u);
           }
           umma_commit_2sm_both(&empty_bar[stage]);
@@ -299,24 +312,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader_tempty0 = mapa_rank(smem_u32(&tempty_bar[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = cluster; tile < num_tiles; tile += n_clusters) {
-      const Tile t = tile_of<MODE>(args, tile);
-      int64_t rows = args.M;
-      __nv_bfloat16* out = args.out0;
-      if constexpr (!kGated) {
-        rows = t.which == 0 ? args.p[0].M : t.which == 1 ? args.p[1].M : args.p[2].M;
-        out = t.which == 0 ? args.p[0].out : t.which == 1 ? args.p[1].out : args.p[2].out;
-      }
-      const int64_t row = (int64_t)t.m * 256 + rank * 128 + quarter * 32 + lane;
-      const bool row_ok = row < rows;
-      const int col0 = kGated ? t.n * 128 + half * 64 : t.n * 256 + half * 128;
+    // the pairs of 16 columns this warp takes: half of the width's
+    const int pieces = args.width / (kGated ? 16 : 32);
+    const int first = half * ((pieces + 1) / 2), count = half == 0 ? (pieces + 1) / 2 : pieces / 2;
+    constexpr int kStep = kGated ? 16 : 32;
+    Tile t;
+    for (int it = 0; tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
+      const int64_t rows = kGated || t.which == 0 ? args.p[0].M : args.p[1].M;
+      __nv_bfloat16* out = kGated || t.which == 0 ? args.p[0].out : t.which == 1 ? args.p[1].out : args.p[2].out;
+      const int half_rows = t.which == 0 ? args.p[0].half_rows : 128;
+      const int64_t row = (int64_t)(2 * t.m + rank) * half_rows + quarter * 32 + lane;
+      const bool row_ok = row < rows && quarter * 32 + lane < half_rows;
+      const int col0 = t.n * args.width + first * kStep;
       const int64_t base = row * args.N + col0;
       // dh of this thread's row, loaded before the accumulator is ready
       [[maybe_unused]] uint4 dhq[MODE == GLU_GRAD ? 8 : 1];
       if constexpr (MODE == GLU_GRAD) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          dhq[q] = row_ok && col0 + 8 * q < args.N ? __ldg(reinterpret_cast<const uint4*>(args.dh + base) + q)
+          dhq[q] = row_ok && q < 2 * count && col0 + 8 * q < args.N ? __ldg(reinterpret_cast<const uint4*>(args.dh + base) + q)
                                                    : make_uint4(0u, 0u, 0u, 0u);
       }
       if (!wait_asleep(&tfull_bar[acc], acc_phase, &abort_s)) {
@@ -327,16 +341,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256;
       // four pairs of 16 columns; the next pair's TMEM loads are in flight while one is worked on
-      const uint32_t ta = t_row + half * (kGated ? 64 : 128), tb = ta + (kGated ? 128 : 16);
-      constexpr int kStep = kGated ? 16 : 32;
+      const uint32_t ta = t_row + first * kStep, tb = ta + (kGated ? args.width : 16);
       uint32_t ra[2][16], rb[2][16];
       tmem_ld_x16(ta, ra[0]);
       tmem_ld_x16(tb, rb[0]);
       tmem_ld_wait16(ra[0], rb[0]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        if (k >= count) break;
         const int cur = k & 1;
-        if (k + 1 < 4) {
+        if (k + 1 < count) {
           tmem_ld_x16(ta + (k + 1) * kStep, ra[cur ^ 1]);
           tmem_ld_x16(tb + (k + 1) * kStep, rb[cur ^ 1]);
         }
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok) {
             store16(out + at, o0, col, args.N, args.wide);
             if constexpr (MODE == GLU_GRAD) {
-              store16(args.out1 + at, o1, col, args.N, args.wide);
+              store16(args.du + at, o1, col, args.N, args.wide);
               if (args.h != nullptr) store16(args.h + at, o2, col, args.N, args.wide);
             }
           }
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             store16(out + at + 16, o1, col + 16, args.N, args.wide);
           }
         }
-        if (k + 1 < 4) tmem_ld_wait16(ra[cur ^ 1], rb[cur ^ 1]);
+        if (k + 1 < count) tmem_ld_wait16(ra[cur ^ 1], rb[cur ^ 1]);
       }
       tc_fence_before();
       __syncwarp();
@@ -412,7 +426,7 @@ struct Maps {
 };
 
 template <int MODE, int ACT>
-cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int64_t tiles, unsigned* status, cudaStream_t s) {
+cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
   auto kern = glu_gemm_kernel<MODE, ACT>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
@@ -424,10 +438,8 @@ cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int64_t tiles, u
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  const int clusters = (int)std::min<int64_t>(tiles, num_sms() / 2);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
+  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
@@ -440,26 +452,72 @@ cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int64_t tiles, u
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, args, (int)tiles, status);
+  return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, args, status);
 }
 
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
 bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-// g and u of N tokens: the tensor maps and the tile grid of GLU_FWD and GLU_GRAD.
-bool gated_args(const void* W_gate, const void* W_up, const void* x, int64_t N, int D, int H, Maps& m,
-                GluGemmArgs& a) {
+// Deals out n_long tiles of `a` k-blocks and n_short of `b` ≤ a to `pairs` CTA pairs (GluGemmArgs); returns the
+// longest share in k-blocks, each tile with kTileCost more (its accumulator's turn-over, measured at
+// about 3000 cycles, six k-blocks).
+constexpr int kTileCost = 6;
+int64_t deal(int64_t n_long, int a, int64_t n_short, int b, int pairs, GluGemmArgs& g) {
+  g.n_long = (int)n_long;
+  g.n_short = (int)n_short;
+  g.rest = (int)(n_long % pairs);
+  const int others = pairs - g.rest;
+  a += kTileCost;
+  b += kTileCost;
+  g.extra = g.rest == 0 || n_short == 0 ? 0 : (int)std::min<int64_t>(a / b, n_short / others);
+  const int64_t turns = n_long / pairs, left = n_short - (int64_t)g.extra * others;
+  const int64_t again = left / pairs, more = left % pairs;
+  const int64_t late = turns * a + (g.extra + again + (more > 0 ? 1 : 0)) * (int64_t)b;
+  const int64_t early = (turns + 1) * a + (again + (more > others ? 1 : 0)) * (int64_t)b;
+  return g.rest == 0 ? late : std::max(late, early);
+}
+
+// The tile width in steps of `step` up to `most` with the shortest longest share, a k-block's cost
+// being what it loads, half_rows of A and half the width's rows of B for each CTA. (A width that leaves few
+// columns over and fills the last turn; at equal cost the wider.)
+template <class F> int best_width(int cols, int most, int step, int half_rows, F share) {
+  int best = most;
+  double least = 0;
+  for (int w = most; w >= std::max(step, most / 4); w -= step) {
+    const double c = share(tiles_of(cols, w)) * (half_rows / 128.0 + (double)w / most);
+    if (w == most || c < 0.97 * least) {
+      best = w;
+      least = c;
+    }
+  }
+  return best;
+}
+
+GluProduct product(int64_t rows, int k_blocks, void* out) {
+  const int tiles = tiles_of(rows, 256);
+  return {rows, tiles, 8 * tiles_of(rows, 16 * tiles), k_blocks, static_cast<__nv_bfloat16*>(out)};
+}
+
+// g and u of N tokens: the tensor maps and the tiles of GLU_FWD and GLU_GRAD.
+bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, int64_t N, int D, int H, Maps& m,
+                GluGemmArgs& a, int& pairs) {
+  a = GluGemmArgs{};
+  a.N = H;
+  a.p[0] = product(N, tiles_of(D, BK), out);
+  const int room = num_sms() / 2;
+  a.width = best_width(H, 128, 16, a.p[0].half_rows, [&](int tiles_n) {
+    return (double)deal((int64_t)a.p[0].tiles_m * tiles_n, a.p[0].k_blocks, 0, 0, room, a);
+  });
+  a.tiles_n = tiles_of(H, a.width);
+  const int64_t tiles = (int64_t)a.p[0].tiles_m * a.tiles_n;
+  if (tiles > INT32_MAX / 2) return false;
+  pairs = (int)std::min<int64_t>(tiles, room);
+  deal(tiles, a.p[0].k_blocks, 0, 0, pairs, a);
   const uint64_t row = (uint64_t)D * 2;
-  if (!make_map_2d(&m.a0, x, D, N, row, BK, 128) || !make_map_2d(&m.b0, W_gate, D, H, row, BK, 128) ||
-      !make_map_2d(&m.b1, W_up, D, H, row, BK, 128))
+  if (!make_map_2d(&m.a0, x, D, N, row, BK, a.p[0].half_rows) || !make_map_2d(&m.b0, W_gate, D, H, row, BK, a.width) ||
+      !make_map_2d(&m.b1, W_up, D, H, row, BK, a.width))
     return false;
   m.a1 = m.c0 = m.c1 = m.x = m.a0;  // (not read)
-  a = GluGemmArgs{};
-  a.M = N;
-  a.N = H;
-  a.tiles_m = tiles_of(N, 256);
-  a.tiles_n = tiles_of(H, 128);
-  a.k_blocks = tiles_of(D, BK);
   return true;
 }
 
@@ -470,12 +528,11 @@ cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void*
   if (N <= kGluFewTokens) return launch_glu_few(W_gate, W_up, x, h, (int)N, D, H, act, s);
   Maps m;
   GluGemmArgs a;
-  if (!gated_args(W_gate, W_up, x, N, D, H, m, a)) return cudaErrorInvalidValue;
-  a.out0 = static_cast<__nv_bfloat16*>(h);
+  int pairs;
+  if (!gated_args(W_gate, W_up, x, h, N, D, H, m, a, pairs)) return cudaErrorInvalidValue;
   a.wide = H % 16 == 0 && on32(h);
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  return act == kActGelu ? launch_mode<GLU_FWD, kActGelu>(m, a, tiles, status, s)
-                         : launch_mode<GLU_FWD, kActSilu>(m, a, tiles, status, s);
+  return act == kActGelu ? launch_mode<GLU_FWD, kActGelu>(m, a, pairs, status, s)
+                         : launch_mode<GLU_FWD, kActSilu>(m, a, pairs, status, s);
 }
 
 cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStream_t s) {
@@ -484,37 +541,45 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
   // dg, du (and h) from x, the weights and dh
   Maps m;
   GluGemmArgs a;
-  if (!gated_args(b.W_gate, b.W_up, b.x, N, D, H, m, a)) return cudaErrorInvalidValue;
-  a.out0 = static_cast<__nv_bfloat16*>(b.dg);
-  a.out1 = static_cast<__nv_bfloat16*>(b.du);
+  int pairs;
+  if (!gated_args(b.W_gate, b.W_up, b.x, b.dg, N, D, H, m, a, pairs)) return cudaErrorInvalidValue;
+  a.du = static_cast<__nv_bfloat16*>(b.du);
   a.h = static_cast<__nv_bfloat16*>(b.h);
   a.dh = static_cast<const __nv_bfloat16*>(b.dh);
   a.wide = H % 16 == 0 && on32(b.dg) && on32(b.du) && on32(b.h);
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, tiles, status, s)
-                                    : launch_mode<GLU_GRAD, kActSilu>(m, a, tiles, status, s);
+  cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, pairs, status, s)
+                                    : launch_mode<GLU_GRAD, kActSilu>(m, a, pairs, status, s);
   if (e != cudaSuccess) return e;
   // dx = dg W_g + du W_u, dW_g = dgᵀ x, dW_u = duᵀ x
   const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)H * 2;
-  if (!make_map_2d(&m.a0, b.dg, H, N, rowH, BK, 128) || !make_map_2d(&m.a1, b.du, H, N, rowH, BK, 128) ||
+  GluGemmArgs w{};
+  w.N = D;
+  w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);
+  w.kb_half = tiles_of(H, BK);
+  w.p[0] = product(N, 2 * w.kb_half, b.dx);
+  w.p[1] = product(H, tiles_of(N, BK), b.dW_gate);
+  w.p[2] = product(H, tiles_of(N, BK), b.dW_up);
+  w.p[1].half_rows = w.p[2].half_rows = 128;  // (read in boxes of 64 columns)
+  if (!make_map_2d(&m.a0, b.dg, H, N, rowH, BK, w.p[0].half_rows) ||
+      !make_map_2d(&m.a1, b.du, H, N, rowH, BK, w.p[0].half_rows) ||
       !make_map_2d(&m.b0, b.W_gate, D, H, rowD, 64, BK) || !make_map_2d(&m.b1, b.W_up, D, H, rowD, 64, BK) ||
       !make_map_2d(&m.c0, b.dg, H, N, rowH, 64, BK) || !make_map_2d(&m.c1, b.du, H, N, rowH, 64, BK) ||
       !make_map_2d(&m.x, b.x, D, N, rowD, 64, BK))
     return cudaErrorInvalidValue;
-  GluGemmArgs w{};
-  w.N = D;
-  w.tiles_n = tiles_of(D, 256);
-  w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);
-  w.kb_half = tiles_of(H, BK);
-  const GluProduct dx{N, tiles_of(N, 256), 2 * w.kb_half, static_cast<__nv_bfloat16*>(b.dx)};
-  const GluProduct dwg{H, tiles_of(H, 256), tiles_of(N, BK), static_cast<__nv_bfloat16*>(b.dW_gate)};
-  GluProduct dwu = dwg;
-  dwu.out = static_cast<__nv_bfloat16*>(b.dW_up);
-  w.dx = dx.k_blocks >= dwg.k_blocks ? 0 : 2;
-  w.p[w.dx] = dx;
-  w.p[w.dx == 0 ? 1 : 0] = dwg;
-  w.p[w.dx == 0 ? 2 : 1] = dwu;
-  return launch_mode<GLU_WIDE, kActGelu>(m, w, (int64_t)(dx.tiles_m + 2 * dwg.tiles_m) * w.tiles_n, status, s);
+  w.dw_first = w.p[1].k_blocks > w.p[0].k_blocks;
+  const auto share = [&](int tiles_n, int room) {
+    const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n, n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n;
+    return w.dw_first ? deal(n_dw, w.p[1].k_blocks, n_dx, w.p[0].k_blocks, room, w)
+                      : deal(n_dx, w.p[0].k_blocks, n_dw, w.p[1].k_blocks, room, w);
+  };
+  const int room = num_sms() / 2;
+  w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)share(tiles_n, room); });
+  w.tiles_n = tiles_of(D, w.width);
+  const int64_t tiles = (int64_t)(w.p[0].tiles_m + 2 * w.p[1].tiles_m) * w.tiles_n;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  pairs = (int)std::min<int64_t>(tiles, room);
+  share(w.tiles_n, pairs);
+  return launch_mode<GLU_WIDE, kActGelu>(m, w, pairs, status, s);
 }
 
 }  // namespace rglru
