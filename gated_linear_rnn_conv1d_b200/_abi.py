@@ -139,6 +139,23 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+_calls = None
+
+
+def calls():
+    """The compiled short way to the calls of a few microseconds (csrc/calls.cpp)."""
+    global _calls
+    if _calls is None:
+        load()
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or was built for another PyTorch: build it with "
+                               "`python -m gated_linear_rnn_conv1d_b200.build`") from e
+        _calls = module
+    return _calls
+
+
 def check(fn: str, code: int) -> None:
     if code != 0:
         lib = load()

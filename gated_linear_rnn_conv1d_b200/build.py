@@ -1,9 +1,9 @@
-"""Builds librglru.so (the sm_100a kernels and the C ABI) in-tree with nvcc.
+"""Builds librglru.so (the sm_100a kernels and the C ABI) and _calls.so (the binding's compiled short
+way, csrc/calls.cpp) in-tree with nvcc and g++.
 
     python -m gated_linear_rnn_conv1d_b200.build [--force]
 
-Objects go to gated_linear_rnn_conv1d_b200/_build/, the library to
-gated_linear_rnn_conv1d_b200/librglru.so. A source is recompiled when it or any
+Objects go to gated_linear_rnn_conv1d_b200/_build/, the libraries next to it. A source is recompiled when it or any
 header under csrc/ or include/ is newer than its object.
 """
 from __future__ import annotations
@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librglru.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -56,6 +58,24 @@ def _compile(src: str, force: bool) -> str:
     return obj
 
 
+def _build_calls(force: bool) -> None:
+    import torch
+    src = os.path.join(CSRC, "calls.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "rglru.h"), torch.version.__file__))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cmd = ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden"]
+    cmd += [f"-I{d}" for d in inc] + [src, "-o", CALLS, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
+                                      "-lc10", "-lc10_cuda", "-L" + PKG, "-l:librglru.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
@@ -67,6 +87,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_calls(force)
     if verbose:
         print(LIB)
     return LIB

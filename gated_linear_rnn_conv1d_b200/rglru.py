@@ -629,7 +629,7 @@ def _check(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device: int) -
     raise ValueError(f"{name}: librglru takes contiguous tensors only")
 
 
-# The current stream's handle without a Stream object around it (3 µs of a decode call's ten).
+# The current stream's handle without a Stream object around it.
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -673,6 +673,10 @@ def glu_forward(W_gate: torch.Tensor, W_up: torch.Tensor, x: torch.Tensor, *, ac
                 h: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_glu_forward: h = act(x W_gateᵀ) ⊙ (x W_upᵀ), x [..., D] → h [..., H], bf16; activation
     'gelu' (exact) or 'silu'."""
+    if stream is None:  # the short way, where nothing is amiss
+        r = _abi.calls().glu_forward(W_gate, W_up, x, _ACT.get(activation, -1), h)
+        if r is not None:
+            return r
     lib = _abi.load()
     dev = _device_of(x)
     H, D = _glu_weights(W_gate, W_up, dev)
@@ -717,6 +721,10 @@ class Act8:
 
 def act8_pack(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None) -> Act8:
     """rglru_act8_pack: x [..., C] (bf16 or float32, C a multiple of 8) → its 8-bit checkpoint."""
+    if stream is None:
+        r = _abi.calls().act8_pack(x)
+        if r is not None:
+            return Act8(*r, x.dtype)
     lib = _abi.load()
     dev = _device_of(x)
     io, shape = _io(x), x.shape
@@ -738,6 +746,10 @@ def act8_pack(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None) ->
 def act8_unpack(a: Act8, *, x: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_act8_unpack: the activation x̂ that a checkpoint holds, in the type it was packed from."""
+    if stream is None and a.dtype in _DT:
+        r = _abi.calls().act8_unpack(a.codes, a.scales, a.dtype is torch.bfloat16, x)
+        if r is not None:
+            return r
     lib = _abi.load()
     dev = _device_of(a.codes)
     C = a.check(dev)
@@ -763,8 +775,13 @@ def glu_backward(W_gate: torch.Tensor, W_up: torch.Tensor, x: Union[torch.Tensor
     """rglru_glu_backward (x a tensor) or rglru_glu_backward_act8 (x a checkpoint of it): the
     gradients of a loss with ∂ℓ/∂h = dh for glu_forward(W_gate, W_up, x). Returns a dict with dx
     [..., D], dW_gate and dW_up [H][D] and, with want_h, the forward's h [..., H] (else None), bf16."""
-    lib = _abi.load()
     packed = isinstance(x, Act8)
+    if stream is None and workspace is None:
+        r = _abi.calls().glu_backward(W_gate, W_up, None if packed else x, x.codes if packed else None,
+                                      x.scales if packed else None, dh, _ACT.get(activation, -1), bool(want_h))
+        if r is not None:
+            return {"dx": r[0], "dW_gate": r[1], "dW_up": r[2], "h": r[3]}
+    lib = _abi.load()
     dev = _device_of(x.codes if packed else x)
     H, D = _glu_weights(W_gate, W_up, dev)
     bf16, lead = torch.bfloat16, x.shape[:-1]
@@ -844,6 +861,10 @@ def w4_quantize(W: torch.Tensor, group: int = 128, *, stream: Optional[torch.cud
 def w4_linear(w: W4Weight, x: torch.Tensor, *, y: Optional[torch.Tensor] = None,
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_w4_linear: y = x Ŵᵀ, x [..., K] bf16 of at most 64 rows → y [..., N] bf16."""
+    if stream is None:
+        r = _abi.calls().w4_linear(w.codes, w.scales, w.group, x, y)
+        if r is not None:
+            return r
     lib = _abi.load()
     dev = _device_of(x)
     N, K = w.check("w", dev)
@@ -865,6 +886,11 @@ def w4_linear(w: W4Weight, x: torch.Tensor, *, y: Optional[torch.Tensor] = None,
 def w4_glu(w_gate: W4Weight, w_up: W4Weight, x: torch.Tensor, *, activation: str = "gelu",
            h: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """rglru_w4_glu: h = act(x Ŵ_gateᵀ) ⊙ (x Ŵ_upᵀ), x [..., D] bf16 of at most 64 rows → h [..., H]."""
+    if stream is None and w_gate.group == w_up.group:
+        r = _abi.calls().w4_glu(w_gate.codes, w_gate.scales, w_up.codes, w_up.scales, w_gate.group, x,
+                                _ACT.get(activation, -1), h)
+        if r is not None:
+            return r
     lib = _abi.load()
     dev = _device_of(x)
     H, D = w_gate.check("w_gate", dev)
