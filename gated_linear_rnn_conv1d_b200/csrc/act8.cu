@@ -29,7 +29,8 @@ struct Item {
 };
 template <bool kWhole> __device__ __forceinline__ Item item_of(int64_t i, int vp, int v8) {
   if constexpr (kWhole) return {i, i >> 2, true};
-  const int64_t row = i / vp;
+  // (a 64-bit division takes as long as the rest of an item's work)
+  const int64_t row = i < (int64_t)1 << 32 ? (int64_t)((uint32_t)i / (uint32_t)vp) : i / vp;
   const int v = (int)(i - row * vp);
   return {row * v8 + v, i >> 2, v < v8};
 }
@@ -42,7 +43,13 @@ template <> struct Vec8<__nv_bfloat16> {
     f[0] = bf16lo(q.x); f[1] = bf16hi(q.x); f[2] = bf16lo(q.y); f[3] = bf16hi(q.y);
     f[4] = bf16lo(q.z); f[5] = bf16hi(q.z); f[6] = bf16lo(q.w); f[7] = bf16hi(q.w);
   }
-  static __device__ void store(void* p, int64_t vec, const float (&f)[8]) {
+  // the bits of the largest magnitude, as a float32's
+  __device__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+    return max(m & 0xFFFF0000u, m << 16);
+  }
+  static __device__ void store(void* p, int64_t vec, const float (&f)[8], bool) {
     static_cast<uint4*>(p)[vec] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   }
@@ -56,65 +63,103 @@ template <> struct Vec8<float> {
   __device__ void get(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
-  static __device__ void store(void* p, int64_t vec, const float (&f)[8]) {
-    static_cast<float4*>(p)[2 * vec] = make_float4(f[0], f[1], f[2], f[3]);
-    static_cast<float4*>(p)[2 * vec + 1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ uint32_t top() const {
+    uint32_t m = 0;
+    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+  // wide: p is on a 32-byte border, and the eight values make one store of a whole L2 sector
+  static __device__ void store(void* p, int64_t vec, const float (&f)[8], bool wide) {
+    float* d = static_cast<float*>(p) + 8 * vec;
+    if (wide) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+                   "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(d)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(d)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   }
 };
+
+// A thread takes kItems items, a block's width apart, and loads them all before it works on the first.
+template <typename T> constexpr int kItems = sizeof(T) == 2 ? 4 : 2;
 
 template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kThreads8)
     act8_pack_kernel(const void* __restrict__ x, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                      int64_t items, int vp, int v8) {
+  constexpr int U = kItems<T>;
   // items is a multiple of 4, so a group's four lanes are all inside or all outside
-  const int64_t i = (int64_t)blockIdx.x * kThreads8 + threadIdx.x;
-  const bool in = i < items;
-  const Item it = item_of<kWhole>(in ? i : 0, vp, v8);
-  Vec8<T> v;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in && it.real) {
-    v.load(x, it.vec);
-    v.get(f);
-  }
-  uint32_t top = 0;  // magnitudes compare as their bits do; infinities and NaN are above the rest
+  const int64_t first = (int64_t)blockIdx.x * (U * kThreads8) + threadIdx.x;
+  Vec8<T> v[U];
+  Item it[U];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // e + 127: m / 2^e is in [64, 128) for e = ⌊log₂ m⌋ − 6, and one more is needed from 127.5 on,
-  // which rint takes to 128
-  int e = (int)(top >> 23) - 6;
-  if (e >= 0 && __uint_as_float(top) * __uint_as_float((uint32_t)(254 - e) << 23) >= 127.5f) ++e;
-  e = max(e, 0);
-  const bool finite = top < kInfBits;
-  const float inv = finite ? __uint_as_float((uint32_t)(254 - e) << 23) : 0.0f;
-  if (!in) return;
-  if ((threadIdx.x & 3) == 0) scales[it.group] = finite ? (uint8_t)e : (uint8_t)255;
-  if (!it.real) return;
-  uint32_t w[2] = {0u, 0u};
-  if (finite) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j / 4] |= (uint32_t)(__float2int_rn(f[j] * inv) & 0xFF) << (8 * (j % 4));
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * kThreads8;
+    it[u] = item_of<kWhole>(i < items ? i : 0, vp, v8);
+    it[u].real = it[u].real && i < items;
+    if (it[u].real) v[u].load(x, it[u].vec);
   }
-  codes[it.vec] = make_uint2(w[0], w[1]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (it[u].real) v[u].get(f);
+    // magnitudes compare as their bits do; infinities and NaN are above the rest
+    uint32_t top = it[u].real ? v[u].top() : 0u;
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // e + 127: m / 2^e is in [64, 128) for e = ⌊log₂ m⌋ − 6, and one more is needed from 127.5 on,
+    // which rint takes to 128
+    int e = (int)(top >> 23) - 6;
+    if (e >= 0 && __uint_as_float(top) * __uint_as_float((uint32_t)(254 - e) << 23) >= 127.5f) ++e;
+    e = max(e, 0);
+    const bool finite = top < kInfBits;
+    const float inv = finite ? __uint_as_float((uint32_t)(254 - e) << 23) : 0.0f;
+    if (first + u * kThreads8 < items && (threadIdx.x & 3) == 0) scales[it[u].group] = finite ? (uint8_t)e : (uint8_t)255;
+    if (!it[u].real) continue;
+    // x / 2^e plus 1.5·2^23 in one rounding is rint(x / 2^e) in the last bits of the sum
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(fmaf(f[j], inv, 12582912.0f));
+    const uint32_t lo = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+    const uint32_t hi = __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410);
+    codes[it[u].vec] = finite ? make_uint2(lo, hi) : make_uint2(0u, 0u);
+  }
 }
 
 template <typename T, bool kWhole>
 __global__ void __launch_bounds__(kThreads8)
     act8_unpack_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, void* __restrict__ x,
-                       int64_t items, int vp, int v8) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads8 + threadIdx.x;
-  if (i >= items) return;
-  const Item it = item_of<kWhole>(i, vp, v8);
-  if (!it.real) return;
-  const uint2 w = __ldcs(codes + it.vec);
-  const uint32_t e = scales[it.group];
-  // 2^(e − 127): e = 0 is subnormal
-  const float step = e == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e > 0u ? e << 23 : 1u << 22);
-  float f[8];
+                       int64_t items, int vp, int v8, bool wide) {
+  constexpr int U = kItems<T>;
+  const int64_t first = (int64_t)blockIdx.x * (U * kThreads8) + threadIdx.x;
+  Item it[U];
+  uint2 w[U];
+  uint32_t e[U];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j % 4))) * step;
-  Vec8<T>::store(x, it.vec, f);
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = first + u * kThreads8;
+    it[u] = item_of<kWhole>(i < items ? i : 0, vp, v8);
+    it[u].real = it[u].real && i < items;
+    if (it[u].real) {
+      w[u] = __ldcs(codes + it[u].vec);
+      e[u] = scales[it[u].group];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!it[u].real) continue;
+    // 2^(e − 127): e = 0 is subnormal
+    const float step = e[u] == 255u ? __uint_as_float(0x7FC00000u)
+                                    : __uint_as_float(e[u] > 0u ? e[u] << 23 : 1u << 22);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (float)(int8_t)((j < 4 ? w[u].x : w[u].y) >> (8 * (j % 4))) * step;
+    Vec8<T>::store(x, it[u].vec, f, wide);
+  }
 }
 
 }  // namespace
@@ -124,7 +169,8 @@ cudaError_t launch_act8_pack(const void* x, void* codes, void* scales, int64_t r
   const bool whole = C % kGroup == 0;
   const int v8 = C / 8, vp = (C + kGroup - 1) / kGroup * 4;
   const int64_t items = rows * vp;
-  const int64_t blocks = (items + kThreads8 - 1) / kThreads8;
+  const int per_block = kThreads8 * (bf16 ? kItems<__nv_bfloat16> : kItems<float>);
+  const int64_t blocks = (items + per_block - 1) / per_block;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   auto kern = bf16 ? (whole ? act8_pack_kernel<__nv_bfloat16, true> : act8_pack_kernel<__nv_bfloat16, false>)
                    : (whole ? act8_pack_kernel<float, true> : act8_pack_kernel<float, false>);
@@ -138,12 +184,13 @@ cudaError_t launch_act8_unpack(const void* codes, const void* scales, void* x, i
   const bool whole = C % kGroup == 0;
   const int v8 = C / 8, vp = (C + kGroup - 1) / kGroup * 4;
   const int64_t items = rows * vp;
-  const int64_t blocks = (items + kThreads8 - 1) / kThreads8;
+  const int per_block = kThreads8 * (bf16 ? kItems<__nv_bfloat16> : kItems<float>);
+  const int64_t blocks = (items + per_block - 1) / per_block;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   auto kern = bf16 ? (whole ? act8_unpack_kernel<__nv_bfloat16, true> : act8_unpack_kernel<__nv_bfloat16, false>)
                    : (whole ? act8_unpack_kernel<float, true> : act8_unpack_kernel<float, false>);
   kern<<<(unsigned)blocks, kThreads8, 0, s>>>(static_cast<const uint2*>(codes), static_cast<const uint8_t*>(scales),
-                                              x, items, vp, v8);
+                                              x, items, vp, v8, (reinterpret_cast<uintptr_t>(x) & 31u) == 0);
   return cudaGetLastError();
 }
 
