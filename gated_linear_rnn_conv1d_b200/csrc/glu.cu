@@ -204,27 +204,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      // this CTA's half of the tile's columns: `width` weight rows, or in one or two boxes of 64 columns
-      const int half_cols = kGated ? args.width : args.width / 2;
-      const bool two = !kGated && half_cols > 64;
-      const uint32_t b_bytes = kGated ? half_cols * BK * 2 : two ? kBBytes : kBBytes / 2;
-      Tile t;
-      for (int it = 0; ok && tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
-        const int half_rows = t.which == 0 ? args.p[0].half_rows : 128;
-        const int arow = (2 * t.m + (int)rank) * half_rows;
-        const uint32_t bytes = 2 * (half_rows * BK * 2 + b_bytes);
-        const int bcol = kGated ? t.n * args.width : t.n * args.width + (int)rank * half_cols;
-        const bool is_dx = kGated || t.which == 0;
-        const bool second = !kGated && t.which == 2;
-        for (int kb = 0; kb < t.k_blocks; ++kb) {
-          if (!wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s)) { ok = false; break; }
-          uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          const uint32_t lbar = leader_full0 + stage * 8;
+    // The whole warp runs the loop and one lane issues: addresses and coordinates then stay in uniform
+    // registers, where TMA and MMA instructions take them from. A loop of one lane alone moves each of them
+    // over, which cost the MMA warp 572 cycles a k-block whatever the tile's width; now it is 525 for the
+    // widest tile (512 of them the MMAs') and 397 for three quarters of it.
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // this CTA's half of the tile's columns: `width` weight rows, or in one or two boxes of 64 columns
+    const int half_cols = kGated ? args.width : args.width / 2;
+    const bool two = !kGated && half_cols > 64;
+    const uint32_t b_bytes = kGated ? half_cols * BK * 2 : two ? kBBytes : kBBytes / 2;
+    Tile t;
+    for (int it = 0; ok && tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
+      const int half_rows = t.which == 0 ? args.p[0].half_rows : 128;
+      const int arow = (2 * t.m + (int)rank) * half_rows;
+      const uint32_t bytes = 2 * (half_rows * BK * 2 + b_bytes);
+      const int bcol = kGated ? t.n * args.width : t.n * args.width + (int)rank * half_cols;
+      const bool is_dx = kGated || t.which == 0;
+      const bool second = !kGated && t.which == 2;
+      for (int kb = 0; kb < t.k_blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s));
+        if (!ok) break;
+        uint8_t* sa = smem + stage * kStageBytes;
+        uint8_t* sb = sa + kABytes;
+        const uint32_t lbar = leader_full0 + stage * 8;
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
           if constexpr (kGated) {
             tma_load_2d_2sm(sa, &tmA0, lbar, kb * BK, arow);
@@ -243,63 +248,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_2sm(sb, mb, lbar, bcol, kc);
             if (two) tma_load_2d_2sm(sb + kBBytes / 2, mb, lbar, bcol + 64, kc);
           }
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
+        __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
-      if (!ok) { abort_s = 1; atomicOr(status, kStatusTimeout); }
     }
+    if (!ok && lane == 0) { abort_s = 1; atomicOr(status, kStatusTimeout); }
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader CTA only) ----------------
-    if (leader && lane == 0) {
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       const uint32_t idesc = umma_idesc_bf16_f32(256, kGated ? 2 * args.width : args.width);
+      const uint32_t smem0 = smem_u32(smem);
       Tile t;
       for (int it = 0; ok && tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
         const bool a_mn = !kGated && t.which != 0;
-        if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1, &abort_s)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait(&tempty_bar[acc], acc_phase ^ 1, &abort_s));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         for (int kb = 0; kb < t.k_blocks; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, &abort_s)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_s));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * kStageBytes);
+          const uint32_t a_addr = smem0 + stage * kStageBytes;
           const uint32_t b_addr = a_addr + kABytes;
-          // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box
+          // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box (in
+          // units of 16 bytes, the descriptors' start address)
           const uint32_t first = kb == 0 ? 0u : 1u;
-          if (kGated) {
+          const uint64_t a_k = umma_desc_sw128(a_addr), b_k = umma_desc_sw128(b_addr);
+          const uint64_t a_m = umma_desc_sw128_mn(a_addr, kABytes / 2), b_m = umma_desc_sw128_mn(b_addr, kBBytes / 2);
+          if (elect_one()) {
+            if (kGated) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32), umma_desc_sw128(b_addr + k * 32), idesc,
-                           k == 0 ? first : 1u);
-          } else if (a_mn) {
+              for (int k = 0; k < BK / 16; ++k)
+                umma_f16_2sm(d_tmem, a_k + k * 2, b_k + k * 2, idesc, k == 0 ? first : 1u);
+            } else if (a_mn) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_f16_2sm(d_tmem, umma_desc_sw128_mn(a_addr + k * 2048, kABytes / 2),
-                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), idesc | kIdescAMN | kIdescBMN,
-                           k == 0 ? first : 1u);
-          } else {
+              for (int k = 0; k < BK / 16; ++k)
+                umma_f16_2sm(d_tmem, a_m + k * 128, b_m + k * 128, idesc | kIdescAMN | kIdescBMN, k == 0 ? first : 1u);
+            } else {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_f16_2sm(d_tmem, umma_desc_sw128(a_addr + k * 32),
-                           umma_desc_sw128_mn(b_addr + k * 2048, kBBytes / 2), idesc | kIdescBMN,
-                           k == 0 ? first : 1u);
+              for (int k = 0; k < BK / 16; ++k)
+                umma_f16_2sm(d_tmem, a_k + k * 2, b_m + k * 128, idesc | kIdescBMN, k == 0 ? first : 1u);
+            }
+            umma_commit_2sm_both(&empty_bar[stage]);
           }
-          umma_commit_2sm_both(&empty_bar[stage]);
+          __syncwarp();
           if (++stage == kStages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
-        umma_commit_2sm_both(&tfull_bar[acc]);
+        if (elect_one()) umma_commit_2sm_both(&tfull_bar[acc]);
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
-      if (!ok) { abort_s = 1; atomicOr(status, kStatusTimeout); }
+      if (!ok && lane == 0) { abort_s = 1; atomicOr(status, kStatusTimeout); }
       // every MMA issued here has completed before TMEM is freed
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                       smem_u32(&drain_bar))
-                   : "memory");
+      if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&drain_bar))
+                     : "memory");
+      __syncwarp();
       volatile int never = 0;
       (void)mbar_wait(&drain_bar, 0, &never);
     }
