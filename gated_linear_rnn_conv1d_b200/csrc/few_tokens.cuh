@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, RING>::kBlock
   for (int j = 0; j < NT; ++j)
     xrow[j] = a.x + (int64_t)min(8 * j + lane / 4, a.M - 1) * a.K + F::lane_k(lane % 4);
   constexpr int kX = F::template kX<SEG>;
-  constexpr bool kEarly = NT == 1;  // x is loaded a segment ahead
+  constexpr bool kEarly = NT * kX <= 4;  // x is loaded a segment ahead (up to 16 registers)
   typename F::template Ahead<MT, SEG, GLU> next;
   uint4 x_next[NT][kX];
   auto load_x = [&](uint4(&x)[NT][kX], int seg) {
