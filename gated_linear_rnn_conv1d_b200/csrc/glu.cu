@@ -50,6 +50,10 @@ struct GluProduct {
   int tiles_m, half_rows;
   int k_blocks;
   __nv_bfloat16* out;
+  // k may be cut into `splits` pieces of kb_per k-blocks, each a tile of its own that writes its float32 sums
+  // to part [splits][M][N]; a second kernel adds them, in order
+  int splits, kb_per;
+  float* part;
 };
 
 struct GluGemmArgs {
@@ -69,7 +73,7 @@ struct GluGemmArgs {
 };
 
 struct Tile {
-  int m, n, which, k_blocks;
+  int m, n, which, split, kb0, kb1;
 };
 // The it-th tile of a pair; false when it has no more.
 template <int MODE>
@@ -93,12 +97,21 @@ __device__ __forceinline__ bool tile_of(const GluGemmArgs& a, int it, int pair, 
   int tile = (int)at;
   t.which = 0;
   if (MODE == GLU_WIDE && is_long == (a.dw_first != 0)) {  // a tile of dW
-    const int each = a.p[1].tiles_m * a.tiles_n;
+    const int each = a.p[1].tiles_m * a.tiles_n * a.p[1].splits;
     t.which = tile < each ? 1 : 2;
     tile -= tile < each ? 0 : each;
   }
   const int tiles_m = t.which == 0 ? a.p[0].tiles_m : a.p[1].tiles_m;
-  t.k_blocks = t.which == 0 ? a.p[0].k_blocks : a.p[1].k_blocks;
+  t.split = 0;
+  t.kb0 = 0;
+  t.kb1 = t.which == 0 ? a.p[0].k_blocks : a.p[1].k_blocks;
+  if constexpr (MODE == GLU_WIDE) {
+    const int kb_per = t.which == 0 ? a.p[0].kb_per : a.p[1].kb_per;
+    t.split = tile / (tiles_m * a.tiles_n);
+    tile -= t.split * tiles_m * a.tiles_n;
+    t.kb0 = t.split * kb_per;
+    t.kb1 = min(t.kb0 + kb_per, t.kb1);
+  }
   const int band = tile / (kBand * a.tiles_n);
   const int r = tile - band * kBand * a.tiles_n;
   const int rows = min(kBand, tiles_m - band * kBand);
@@ -124,6 +137,13 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16], 
     if (col < cols) *reinterpret_cast<uint4*>(p) = a;
     if (col + 8 < cols) *reinterpret_cast<uint4*>(p + 8) = b;
   }
+}
+
+// (part's rows are multiples of 32 bytes, as D is of eight)
+__device__ __forceinline__ void store8_f32(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // As mbar_wait, the thread asleep between its looks (the epilogue's and the loader's waits are long;
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int bcol = kGated ? t.n * args.width : t.n * args.width + (int)rank * half_cols;
       const bool is_dx = kGated || t.which == 0;
       const bool second = !kGated && t.which == 2;
-      for (int kb = 0; kb < t.k_blocks; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s));
         if (!ok) break;
         uint8_t* sa = smem + stage * kStageBytes;
@@ -271,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = 0; kb < t.k_blocks; ++kb) {
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_s));
           if (!ok) break;
           tc_fence_after();
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b_addr = a_addr + kABytes;
           // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box (in
           // units of 16 bytes, the descriptors' start address)
-          const uint32_t first = kb == 0 ? 0u : 1u;
+          const uint32_t first = kb == t.kb0 ? 0u : 1u;
           const uint64_t a_k = umma_desc_sw128(a_addr), b_k = umma_desc_sw128(b_addr);
           const uint64_t a_m = umma_desc_sw128_mn(a_addr, kABytes / 2), b_m = umma_desc_sw128_mn(b_addr, kBBytes / 2);
           if (elect_one()) {
@@ -410,9 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             o0[j] = __uint_as_float(ra[cur][j]);
             o1[j] = __uint_as_float(rb[cur][j]);
           }
-          if (row_ok) {
+          float* part = t.which == 0 ? args.p[0].part : t.which == 1 ? args.p[1].part : args.p[2].part;
+          if (row_ok && part == nullptr) {
             store16(out + at, o0, col, args.N, args.wide);
             store16(out + at + 16, o1, col + 16, args.N, args.wide);
+          } else if (row_ok) {
+            part += (int64_t)t.split * rows * args.N + at;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (col + 8 * q < args.N) store8_f32(part + 8 * q, &o0[8 * q]);
+              if (col + 16 + 8 * q < args.N) store8_f32(part + 16 + 8 * q, &o1[8 * q]);
+            }
           }
         }
         if (k + 1 < count) tmem_ld_wait16(ra[cur ^ 1], rb[cur ^ 1]);
@@ -431,6 +459,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
                  : "memory");
+  }
+}
+
+// out = Σ part[s] for up to three outputs: eight values a thread, splits added in order.
+struct GluSum {
+  const float* part;
+  __nv_bfloat16* out;
+  int64_t n8;  // vectors of eight
+  int splits;
+};
+struct GluSums {
+  GluSum s[3];
+};
+__global__ void __launch_bounds__(256) glu_sum_kernel(const GluSums a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const GluSum& u = a.s[k];
+    if (i >= 0 && i < u.n8) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const float4* p = reinterpret_cast<const float4*>(u.part) + 2 * i;
+#pragma unroll 4
+      for (int s = 0; s < u.splits; ++s) {
+        const float4 x = __ldcs(p + 2 * u.n8 * s), y = __ldcs(p + 2 * u.n8 * s + 1);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      reinterpret_cast<uint4*>(u.out)[i] = pack8(v);
+    }
+    i -= u.n8;
   }
 }
 
@@ -508,8 +568,53 @@ template <class F> int best_width(int cols, int most, int step, int half_rows, F
 
 GluProduct product(int64_t rows, int k_blocks, void* out) {
   const int tiles = tiles_of(rows, 256);
-  return {rows, tiles, 8 * tiles_of(rows, 16 * tiles), k_blocks, static_cast<__nv_bfloat16*>(out)};
+  return {rows, tiles, 8 * tiles_of(rows, 16 * tiles), k_blocks, static_cast<__nv_bfloat16*>(out), 1, k_blocks, nullptr};
 }
+
+// dx, dW_g and dW_u: the tile width, and in how many pieces of k they are formed. A product whose k-blocks are
+// many more than a pair's share of all the work (few tokens and a long H for dx; many tokens and small
+// weights for dW) is cut into pieces of about that share, at least 16 k-blocks long; the second kernel
+// and the partial sums cost about as much as 16 more. A function of the sizes alone (74 pairs, a B200's),
+// as the workspace holds the partial sums.
+constexpr int kPairs = 74;
+int64_t share_wide(GluGemmArgs& w, int tiles_n, int pairs) {
+  const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n * w.p[0].splits;
+  const int64_t n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n * w.p[1].splits;
+  w.dw_first = w.p[1].kb_per > w.p[0].kb_per;
+  return w.dw_first ? deal(n_dw, w.p[1].kb_per, n_dx, w.p[0].kb_per, pairs, w)
+                    : deal(n_dx, w.p[0].kb_per, n_dw, w.p[1].kb_per, pairs, w);
+}
+int64_t cut_wide(GluGemmArgs& w, int tiles_n) {
+  const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n, n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n;
+  const int64_t all = n_dx * (w.p[0].k_blocks + kTileCost) + n_dw * (w.p[1].k_blocks + kTileCost);
+  const int64_t share = std::max<int64_t>(all / kPairs, 16);
+  int64_t more = 0;
+  for (int i = 0; i < 3; ++i) {
+    GluProduct& p = w.p[i];
+    p.splits = 1;
+    p.kb_per = p.k_blocks;
+    if (4 * (int64_t)p.k_blocks > 5 * share && p.k_blocks >= share + 16) {
+      p.splits = tiles_of(p.k_blocks, (int)share);
+      p.kb_per = tiles_of(p.k_blocks, p.splits);
+      p.splits = tiles_of(p.k_blocks, p.kb_per);
+      more = 16;
+    }
+  }
+  return share_wide(w, tiles_n, kPairs) + more;
+}
+void plan_wide(int64_t N, int D, int H, GluGemmArgs& w) {
+  w = GluGemmArgs{};
+  w.N = D;
+  w.kb_half = tiles_of(H, BK);
+  w.p[0] = product(N, 2 * w.kb_half, nullptr);
+  w.p[1] = product(H, tiles_of(N, BK), nullptr);
+  w.p[1].half_rows = 128;  // (read in boxes of 64 columns)
+  w.p[2] = w.p[1];
+  w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)cut_wide(w, tiles_n); });
+  w.tiles_n = tiles_of(D, w.width);
+  cut_wide(w, w.tiles_n);
+}
+int64_t part_floats(const GluProduct& p, int D) { return p.splits > 1 ? p.splits * p.M * D : 0; }
 
 // g and u of N tokens: the tensor maps and the tiles of GLU_FWD and GLU_GRAD.
 bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, int64_t N, int D, int H, Maps& m,
@@ -565,34 +670,49 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
   if (e != cudaSuccess) return e;
   // dx = dg W_g + du W_u, dW_g = dgᵀ x, dW_u = duᵀ x
   const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)H * 2;
-  GluGemmArgs w{};
-  w.N = D;
+  GluGemmArgs w;
+  plan_wide(N, D, H, w);
   w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);
-  w.kb_half = tiles_of(H, BK);
-  w.p[0] = product(N, 2 * w.kb_half, b.dx);
-  w.p[1] = product(H, tiles_of(N, BK), b.dW_gate);
-  w.p[2] = product(H, tiles_of(N, BK), b.dW_up);
-  w.p[1].half_rows = w.p[2].half_rows = 128;  // (read in boxes of 64 columns)
+  void* const outs[3] = {b.dx, b.dW_gate, b.dW_up};
+  float* part = static_cast<float*>(b.part);
+  GluSums sums{};
+  int64_t vectors = 0;
+  for (int i = 0; i < 3; ++i) {
+    w.p[i].out = static_cast<__nv_bfloat16*>(outs[i]);
+    if (w.p[i].splits == 1) continue;
+    w.p[i].part = part;
+    sums.s[i] = GluSum{part, w.p[i].out, w.p[i].M * D / 8, w.p[i].splits};
+    part += part_floats(w.p[i], D);
+    vectors += sums.s[i].n8;
+  }
   if (!make_map_2d(&m.a0, b.dg, H, N, rowH, BK, w.p[0].half_rows) ||
       !make_map_2d(&m.a1, b.du, H, N, rowH, BK, w.p[0].half_rows) ||
       !make_map_2d(&m.b0, b.W_gate, D, H, rowD, 64, BK) || !make_map_2d(&m.b1, b.W_up, D, H, rowD, 64, BK) ||
       !make_map_2d(&m.c0, b.dg, H, N, rowH, 64, BK) || !make_map_2d(&m.c1, b.du, H, N, rowH, 64, BK) ||
       !make_map_2d(&m.x, b.x, D, N, rowD, 64, BK))
     return cudaErrorInvalidValue;
-  w.dw_first = w.p[1].k_blocks > w.p[0].k_blocks;
-  const auto share = [&](int tiles_n, int room) {
-    const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n, n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n;
-    return w.dw_first ? deal(n_dw, w.p[1].k_blocks, n_dx, w.p[0].k_blocks, room, w)
-                      : deal(n_dx, w.p[0].k_blocks, n_dw, w.p[1].k_blocks, room, w);
-  };
-  const int room = num_sms() / 2;
-  w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)share(tiles_n, room); });
-  w.tiles_n = tiles_of(D, w.width);
-  const int64_t tiles = (int64_t)(w.p[0].tiles_m + 2 * w.p[1].tiles_m) * w.tiles_n;
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  pairs = (int)std::min<int64_t>(tiles, room);
-  share(w.tiles_n, pairs);
-  return launch_mode<GLU_WIDE, kActGelu>(m, w, pairs, status, s);
+  const int64_t tiles = ((int64_t)w.p[0].tiles_m * w.p[0].splits + 2 * (int64_t)w.p[1].tiles_m * w.p[1].splits) * w.tiles_n;
+  if (tiles > INT32_MAX / 2 || (vectors + 255) / 256 > INT32_MAX) return cudaErrorInvalidValue;
+  pairs = (int)std::min<int64_t>(tiles, num_sms() / 2);
+  share_wide(w, w.tiles_n, pairs);
+  e = launch_mode<GLU_WIDE, kActGelu>(m, w, pairs, status, s);
+  if (e != cudaSuccess || vectors == 0) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((vectors + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernel waits (pdl_wait)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, glu_sum_kernel, (const GluSums)sums);
+}
+
+size_t glu_backward_part_bytes(int64_t N, int D, int H) {
+  GluGemmArgs w;
+  plan_wide(N, D, H, w);
+  return (size_t)(part_floats(w.p[0], D) + part_floats(w.p[1], D) + part_floats(w.p[2], D)) * sizeof(float);
 }
 
 }  // namespace rglru

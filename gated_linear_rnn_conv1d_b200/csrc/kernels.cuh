@@ -227,6 +227,7 @@ struct GluBwdArgs {
   const void* dh;      // [N][H]
   void* dg;            // [N][H] scratch
   void* du;            // [N][H] scratch
+  void* part;          // glu_backward_part_bytes(N, D, H) of scratch, 32-byte aligned
   void* dx;            // [N][D]
   void* dW_gate;       // [H][D]
   void* dW_up;
@@ -235,6 +236,7 @@ struct GluBwdArgs {
   int D, H, act;
 };
 cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStream_t s);
+size_t glu_backward_part_bytes(int64_t N, int D, int H);
 // x [rows][C] (bf16 or float32) ↔ int8 codes [rows][C] and scale bytes [rows][⌈C/32⌉]; C a
 // multiple of 8.
 constexpr int kAct8Group = 32;

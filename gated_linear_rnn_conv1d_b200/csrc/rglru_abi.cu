@@ -941,15 +941,16 @@ bool valid_act8(int64_t N, int C) {
 bool valid_w4(int N, int K, int group) {
   return valid_R(N) && valid_R(K) && (group == 32 || group == 64 || group == 128) && K % group == 0;
 }
-// dg [N][H] | du [N][H] | x̂ [N][D] (from_act8), bf16
+// dg [N][H] | du [N][H] | x̂ [N][D] (from_act8), bf16 | partial sums of dx and dW, float32
 struct GluBwdLayout {
-  size_t off_du, off_x, bytes;
+  size_t off_du, off_x, off_part, bytes;
 };
 GluBwdLayout glu_bwd_layout(int64_t N, int D, int H, bool from_act8) {
   GluBwdLayout L;
   L.off_du = round256((size_t)N * H * 2);
   L.off_x = 2 * L.off_du;
-  L.bytes = L.off_x + (from_act8 ? round256((size_t)N * D * 2) : 0);
+  L.off_part = L.off_x + (from_act8 ? round256((size_t)N * D * 2) : 0);
+  L.bytes = L.off_part + round256(glu_backward_part_bytes(N, D, H));
   return L;
 }
 int glu_backward_impl(const void* W_gate, const void* W_up, const void* x, const void* codes, const void* scales,
@@ -979,7 +980,7 @@ int glu_backward_impl(const void* W_gate, const void* W_up, const void* x, const
   }
   GluBwdArgs b{};
   b.W_gate = W_gate; b.W_up = W_up; b.x = x; b.dh = dh;
-  b.dg = workspace; b.du = bytes(workspace) + L.off_du;
+  b.dg = workspace; b.du = bytes(workspace) + L.off_du; b.part = bytes(workspace) + L.off_part;
   b.dx = dx; b.dW_gate = dW_gate; b.dW_up = dW_up; b.h = h;
   b.N = N; b.D = D; b.H = H; b.act = act;
   const cudaError_t e = launch_glu_backward(b, status, s);

@@ -87,6 +87,24 @@ def test_backward(N, D, H, act):
     _check_backward(x, Wg, Wu, dh, act, got)
 
 
+# sums cut into pieces: dx's over the channels (few tokens, long H), dW's over the tokens (small weights),
+# with a last piece that is shorter, and with columns that fill no tile
+@pytest.mark.parametrize("N,D,H", [(17, 72, 4104), (1, 264, 3336), (40, 520, 2056), (5000, 40, 72), (2200, 264, 136)])
+def test_backward_of_long_sums(N, D, H):
+    x, Wg, Wu, dh = _draw(N, D, H, seed=N + 3)
+    plain = 2 * -(-2 * N * H // 256) * 256
+    need = rglru.glu_backward_workspace_bytes(N, D, H)
+    assert need > plain  # room for the pieces
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    dev = [t.to(DEV) for t in (Wg, Wu, x, dh)]
+    got = rglru.glu_backward(*dev, want_h=True, workspace=ws)
+    assert rglru.workspace_status(None) == 0
+    _check_backward(x, Wg, Wu, dh, "gelu", got)
+    for _ in range(3):  # the pieces are added in order
+        again = rglru.glu_backward(*dev, want_h=True)
+        assert all(torch.equal(again[k], got[k]) for k in got)
+
+
 def test_shapes_of_any_rank():
     x, Wg, Wu, dh = _draw(6, 40, 72)
     w = (Wg.to(DEV), Wu.to(DEV))
