@@ -531,17 +531,20 @@ cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsig
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
 bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// What a tile of so many k-blocks costs in k-blocks (of about 0.3 µs): its accumulator changes hands, and
+// where its k is short the epilogue is what it takes (3.6 µs for 256 × 256 of dW with one k-block, of
+// which 2.1 are the stores).
+int tile_cost(int k_blocks) { return std::max(k_blocks + 2, 12); }
+
 // Deals out n_long tiles of `a` k-blocks and n_short of `b` ≤ a to `pairs` CTA pairs (GluGemmArgs); returns the
-// longest share in k-blocks, each tile with kTileCost more (its accumulator's turn-over, measured at
-// about 3000 cycles, six k-blocks).
-constexpr int kTileCost = 6;
+// longest share.
 int64_t deal(int64_t n_long, int a, int64_t n_short, int b, int pairs, GluGemmArgs& g) {
   g.n_long = (int)n_long;
   g.n_short = (int)n_short;
   g.rest = (int)(n_long % pairs);
   const int others = pairs - g.rest;
-  a += kTileCost;
-  b += kTileCost;
+  a = tile_cost(a);
+  b = tile_cost(b);
   g.extra = g.rest == 0 || n_short == 0 ? 0 : (int)std::min<int64_t>(a / b, n_short / others);
   const int64_t turns = n_long / pairs, left = n_short - (int64_t)g.extra * others;
   const int64_t again = left / pairs, more = left % pairs;
@@ -586,7 +589,7 @@ int64_t share_wide(GluGemmArgs& w, int tiles_n, int pairs) {
 }
 int64_t cut_wide(GluGemmArgs& w, int tiles_n) {
   const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n, n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n;
-  const int64_t all = n_dx * (w.p[0].k_blocks + kTileCost) + n_dw * (w.p[1].k_blocks + kTileCost);
+  const int64_t all = n_dx * tile_cost(w.p[0].k_blocks) + n_dw * tile_cost(w.p[1].k_blocks);
   const int64_t share = std::max<int64_t>(all / kPairs, 16);
   int64_t more = 0;
   for (int i = 0; i < 3; ++i) {
