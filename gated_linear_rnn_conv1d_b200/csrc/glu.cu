@@ -28,11 +28,16 @@ namespace rglru {
 namespace {
 
 constexpr int BK = 64;  // 64 bf16 = one 128-byte swizzle row
-constexpr int kStages = 6;
+constexpr int kMaxStages = 16;
 constexpr int kABytes = 128 * BK * 2;  // this CTA's 128 rows of A
 constexpr int kBBytes = 128 * BK * 2;  // this CTA's half of the B tile
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024;
+// The ring: as many stages as fit, each of the rows that are loaded (seven of the largest; few tokens and
+// narrow tiles have up to 16: the bytes in flight are what HBM's latency asks for. Of weights that are not in
+// L2, D 4096, H 12288, 64 tokens take 51.3 µs and 57.3 with six stages of the largest; 256 tokens 57.3 and
+// 61.3; from 2048 tokens on there is no difference). An MMA reads 128 rows of A whatever was loaded: up
+// to kABytes from a stage's start have to be there.
+constexpr int kRingBytes = 7 * (kABytes + kBBytes);
+constexpr int kSmem = kRingBytes + 1024;
 constexpr int kTmemCols = 512;  // two 256-column accumulators
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -58,6 +63,7 @@ struct GluProduct {
 
 struct GluGemmArgs {
   int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
+  int stages, stage_bytes, b_at;  // the ring; B's place in a stage
   int tiles_n, width;  // of every product; width: channels (up to 128), or columns (up to 256)
   int wide;            // rows of every matrix stored start on 32-byte borders
   __nv_bfloat16* du;          // GLU_GRAD
@@ -168,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // X x (for dW, in boxes of 64 columns).
   constexpr bool kGated = MODE != GLU_WIDE;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[kStages];
-  __shared__ __align__(8) uint64_t empty_bar[kStages];
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_clusters = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < args.stages; ++i) {
       mbar_init(&full_bar[i], 1);
       mbar_init(&empty_bar[i], 1);
     }
@@ -246,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s));
         if (!ok) break;
-        uint8_t* sa = smem + stage * kStageBytes;
-        uint8_t* sb = sa + kABytes;
+        uint8_t* sa = smem + stage * args.stage_bytes;
+        uint8_t* sb = sa + args.b_at;
         const uint32_t lbar = leader_full0 + stage * 8;
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
+        if (++stage == args.stages) { stage = 0; phase ^= 1; }
       }
     }
     if (!ok && lane == 0) { abort_s = 1; atomicOr(status, kStatusTimeout); }
@@ -295,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_s));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem0 + stage * kStageBytes;
-          const uint32_t b_addr = a_addr + kABytes;
+          const uint32_t a_addr = smem0 + stage * args.stage_bytes;
+          const uint32_t b_addr = a_addr + args.b_at;
           // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box (in
           // units of 16 bytes, the descriptors' start address)
           const uint32_t first = kb == t.kb0 ? 0u : 1u;
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_2sm_both(&empty_bar[stage]);
           }
           __syncwarp();
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+          if (++stage == args.stages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
         if (elect_one()) umma_commit_2sm_both(&tfull_bar[acc]);
@@ -536,6 +542,14 @@ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 // which 2.1 are the stores).
 int tile_cost(int k_blocks) { return std::max(k_blocks + 2, 12); }
 
+// The ring for stages of a_rows rows of A and b_bytes of B (multiples of 1024 bytes).
+void set_ring(GluGemmArgs& g, int a_rows, int b_bytes) {
+  g.b_at = a_rows * BK * 2;
+  g.stage_bytes = g.b_at + b_bytes;
+  // (the last stage's A is read to kABytes from its start)
+  g.stages = std::min(kMaxStages, (kRingBytes - std::max(0, kABytes - g.stage_bytes)) / g.stage_bytes);
+}
+
 // Deals out n_long tiles of `a` k-blocks and n_short of `b` ≤ a to `pairs` CTA pairs (GluGemmArgs); returns the
 // longest share.
 int64_t deal(int64_t n_long, int a, int64_t n_short, int b, int pairs, GluGemmArgs& g) {
@@ -615,6 +629,7 @@ void plan_wide(int64_t N, int D, int H, GluGemmArgs& w) {
   w.p[2] = w.p[1];
   w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)cut_wide(w, tiles_n); });
   w.tiles_n = tiles_of(D, w.width);
+  set_ring(w, 128, w.width > 128 ? kBBytes : kBBytes / 2);
   cut_wide(w, w.tiles_n);
 }
 int64_t part_floats(const GluProduct& p, int D) { return p.splits > 1 ? p.splits * p.M * D : 0; }
@@ -630,6 +645,7 @@ bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, 
     return (double)deal((int64_t)a.p[0].tiles_m * tiles_n, a.p[0].k_blocks, 0, 0, room, a);
   });
   a.tiles_n = tiles_of(H, a.width);
+  set_ring(a, a.p[0].half_rows, a.width * BK * 2);
   const int64_t tiles = (int64_t)a.p[0].tiles_m * a.tiles_n;
   if (tiles > INT32_MAX / 2) return false;
   pairs = (int)std::min<int64_t>(tiles, room);
