@@ -8,12 +8,12 @@
 
 namespace rglru {
 namespace {
-// Up to eight tokens chunks of one granule and a ring of four are as fast as any (35 µs for 201 MB;
-// wider chunks or deeper rings 36 to 47 µs: x is read through what shared memory leaves of the L1); with
-// sixteen, x weighs twice as much and is shared by the chunk's two granules (39 µs against 47 µs).
+// The copies are three or four steps of one granule ahead. 201 MB of weights, eight tokens: chunks of 1, 2, 3 and 6
+// granules 34.2, 32.4, 32.0 and 33.0 µs (a chunk shares the loads of x, which are read through what shared
+// memory leaves of the L1); sixteen: 33.3 and 33.8 µs for 2 and 3.
 template <int ACT> cudaError_t launch_act(const FewArgs& a, cudaStream_t s) {
-  return a.M <= 8 ? launch_few<FewBf16, true, ACT, 1, 1, 128, 4>(a, s)
-                  : launch_few<FewBf16, true, ACT, 2, 2, 128, 2>(a, s);
+  return a.M <= 8 ? launch_few<FewBf16, true, ACT, 1, 3, 128, 1, 5>(a, s)
+                  : launch_few<FewBf16, true, ACT, 2, 2, 128, 1, 4>(a, s);
 }
 }  // namespace
 

@@ -15,18 +15,29 @@ namespace {
 
 template <int GROUP, bool GLU, int ACT> cudaError_t launch_group(const FewArgs& a, cudaStream_t s) {
   using F = FewW4<GROUP>;
-  // Wide chunks share the loads and shuffles of x between their granules (12288 gated channels of 4096
-  // inputs, eight tokens: 25, 21 and 19 µs for chunks of 1, 2 and 4; sixteen: 40, 29 and 27 µs), where
-  // every block has so many granules.
-  const int each = (a.rows + (GLU ? 7 : 15)) / (GLU ? 8 : 16) / (2 * num_sms());
-  if (a.M <= 8)
-    return each >= 2   ? launch_few<F, GLU, ACT, 1, 4, 64, 2>(a, s)
-           : each >= 1 ? launch_few<F, GLU, ACT, 1, 2, 64, 3>(a, s)
-                       : launch_few<F, GLU, ACT, 1, 1, 64, 4>(a, s);
-  if (a.M <= 16)
-    return each >= 2 ? launch_few<F, GLU, ACT, 2, 4, 64, 2>(a, s) : launch_few<F, GLU, ACT, 2, 1, 64, 4>(a, s);
-  if (a.M <= 32) return launch_few<F, GLU, ACT, 4, 1, 64, 4>(a, s);
-  return launch_few<F, GLU, ACT, 8, 1, 64, 4>(a, s);
+  // A chunk takes all of a block's granules where it can: x and its order are then formed once, and a ring step of
+  // up to three granules has its bookkeeping once. K = 4096, G = 128, eight tokens, chunks of 1, 2, 3
+  // and 6 granules: one granule a block (4096 rows) 3.9, 4.3, 4.5 and 4.9 µs; two (8192) 6.6, 5.6, 5.7 and 6.2;
+  // three (12288) 9.6, 8.8, 6.9 and 7.5; five (20480) 15.0, 13.1, 11.4 and 9.8; sixteen tokens alike.
+  const int granules = (a.rows + (GLU ? 7 : 15)) / (GLU ? 8 : 16);
+  auto per = [&](int blocks) { return (granules + blocks - 1) / blocks; };
+  if (a.M <= 16) {
+    const int n = per(2 * num_sms());
+    if (a.M <= 8)
+      return n == 1   ? launch_few<F, GLU, ACT, 1, 1, 64, 1, 4>(a, s)
+             : n == 2 ? launch_few<F, GLU, ACT, 1, 2, 64, 2, 2>(a, s)
+             : n == 3 ? launch_few<F, GLU, ACT, 1, 3, 64, 3, 2>(a, s)
+                      : launch_few<F, GLU, ACT, 1, 6, 64, 3, 2>(a, s);
+    return n == 1   ? launch_few<F, GLU, ACT, 2, 1, 64, 1, 4>(a, s)
+           : n == 2 ? launch_few<F, GLU, ACT, 2, 2, 64, 2, 2>(a, s)
+           : n == 3 ? launch_few<F, GLU, ACT, 2, 3, 64, 3, 2>(a, s)
+                    : launch_few<F, GLU, ACT, 2, 6, 64, 3, 2>(a, s);
+  }
+  // Up to 32 tokens one block an SM (4096 rows 7.1 and 8.4 µs for chunks of 2 and 6, 8192 rows 13.4 and 11.3); more
+  // tokens are two halves, each of half the blocks (12288 gated channels, 64 tokens: 68 µs, and 133 with
+  // all their sums in one block's registers).
+  return per(num_sms()) <= 2 ? launch_few<F, GLU, ACT, 4, 2, 64, 2, 4>(a, s)
+                             : launch_few<F, GLU, ACT, 4, 6, 64, 3, 3>(a, s);
 }
 
 template <bool GLU, int ACT> cudaError_t launch_any(const FewArgs& a, int group, cudaStream_t s) {
@@ -38,8 +49,10 @@ template <bool GLU, int ACT> cudaError_t launch_any(const FewArgs& a, int group,
   }
 }
 
-FewArgs few_args(const W4Matrix& w0, const W4Matrix& w1, const void* x, void* out, int M, int rows, int K) {
+FewArgs few_args(const W4Matrix& w0, const W4Matrix& w1, const void* x, void* out, int M, int rows, int K,
+                 int group) {
   FewArgs a{};
+  a.row_groups = K / group;
   a.w0 = static_cast<const uint8_t*>(w0.codes);
   a.w1 = static_cast<const uint8_t*>(w1.codes);
   a.scales0 = static_cast<const __nv_bfloat16*>(w0.scales);
@@ -107,12 +120,12 @@ cudaError_t launch_w4_quantize(const void* w, void* codes, void* scales, int64_t
 
 cudaError_t launch_w4_linear(const W4Matrix& w, const void* x, void* y, int M, int rows, int K, int group,
                              cudaStream_t s) {
-  return launch_any<false, kActGelu>(few_args(w, w, x, y, M, rows, K), group, s);
+  return launch_any<false, kActGelu>(few_args(w, w, x, y, M, rows, K, group), group, s);
 }
 
 cudaError_t launch_w4_glu(const W4Matrix& gate, const W4Matrix& up, const void* x, void* h, int M, int rows, int K,
                           int group, int act, cudaStream_t s) {
-  const FewArgs a = few_args(gate, up, x, h, M, rows, K);
+  const FewArgs a = few_args(gate, up, x, h, M, rows, K, group);
   return act == kActGelu ? launch_any<true, kActGelu>(a, group, s) : launch_any<true, kActSilu>(a, group, s);
 }
 

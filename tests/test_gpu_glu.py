@@ -76,6 +76,16 @@ def test_forward(N, D, H, act):
     _check_forward(x, Wg, Wu, act, h)
 
 
+# one token to sixteen: the channels of a block of the streaming kernel are two, four and nine granules of eight
+@pytest.mark.parametrize("N,D,H", [(1, 72, 4744), (8, 200, 9480), (3, 136, 20008), (9, 72, 4744), (16, 328, 20008)])
+def test_few_tokens_of_many_channels(N, D, H):
+    x, Wg, Wu, _ = _draw(N, D, H, seed=N)
+    h, untouched = _guarded((N, H))
+    rglru.glu_forward(Wg.to(DEV), Wu.to(DEV), x.to(DEV), activation="gelu", h=h)
+    assert untouched()
+    _check_forward(x, Wg, Wu, "gelu", h)
+
+
 @pytest.mark.parametrize("N,D,H", SHAPES)
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 def test_backward(N, D, H, act):

@@ -6,7 +6,7 @@ import torch
 from gated_linear_rnn_conv1d_b200 import rglru
 from oracle import feed_forward as ff
 
-from _glu import ACT, HALF, TINY, w4_bound
+from _glu import ACT, HALF, SUM, TINY, w4_bound
 from _util import f64
 
 pytestmark = pytest.mark.gpu
@@ -66,6 +66,44 @@ def test_glu(M, H, group, K, act):
     err = np.abs(f64(h) - a * u)
     print(f"worst error / bound {np.max(err / bound):.3f}")
     assert (err <= bound).all()
+
+
+def _dense_here(w):
+    """Ŵ in float64 on the GPU: the codes and scales are exact in it."""
+    q = torch.stack([w.codes & 15, w.codes >> 4], 2).view(w.codes.shape[0], -1).double() - 8
+    return q * w.scales.double().repeat_interleave(w.group, 1)
+
+
+# With more rows than the SMs take at once a block has two, three and more granules of 16 rows, in one chunk and in
+# several; the last has eight rows. K: one panel of scales and several, the last of them short.
+@pytest.mark.parametrize("M", [1, 8, 13, 31, 47])
+@pytest.mark.parametrize("N,K,group", [(4744, 288, 32), (9480, 2176, 32), (14216, 4224, 64), (14216, 8320, 128),
+                                       (38008, 192, 64), (38008, 2080, 32)])
+def test_linear_of_many_rows(M, N, K, group):
+    g = torch.Generator(DEV).manual_seed(N + K)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=DEV)
+    scales = (torch.exp(torch.randn(N, K // group, generator=g, device=DEV)) / (8 * K ** 0.5)).to(BF)
+    w, x = rglru.W4Weight(codes, scales, group), _x(M, K, seed=M).to(DEV)
+    buf = torch.full((M * N + 64,), -7.0, dtype=BF, device=DEV)
+    y = rglru.w4_linear(w, x, y=buf[32:32 + M * N].view(M, N))
+    assert (buf[:32] == -7).all() and (buf[32 + M * N:] == -7).all()
+    W = _dense_here(w)
+    ref = x.double() @ W.T
+    ref, e = f64(ref), (K + 16) * SUM * f64(x.double().abs() @ W.abs().T)  # (as w4_bound)
+    bound = (e + HALF * (np.abs(ref) + e)) * (1 + 1e-6) + TINY
+    err = np.abs(f64(y) - ref)
+    print(f"worst error / bound {np.max(err / bound):.3f}")
+    assert (err <= bound).all()
+    # the gated form on the same rows as both matrices' halves
+    H = N // 2 // 8 * 8
+    wg = rglru.W4Weight(codes[:H], scales[:H], group)
+    wu = rglru.W4Weight(codes[N - H:], scales[N - H:], group)
+    h = rglru.w4_glu(wg, wu, x)
+    gg, uu, eg, eu = ref[:, :H], ref[:, N - H:], e[:, :H], e[:, N - H:]
+    a = ff.act(gg, "gelu")
+    ea = 1.13 * eg + ACT * (np.abs(gg) + eg)
+    e = ea * np.abs(uu) + (np.abs(a) + ea) * eu
+    assert (np.abs(f64(h) - a * uu) <= (e + HALF * (np.abs(a * uu) + e)) * (1 + 1e-6) + TINY).all()
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
