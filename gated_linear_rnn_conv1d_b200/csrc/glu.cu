@@ -65,7 +65,8 @@ struct GluGemmArgs {
   int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
   int stages, stage_bytes, b_at;  // the ring; B's place in a stage
   int tiles_n, width;  // of every product; width: channels (up to 128), or columns (up to 256)
-  int wide;            // rows of every matrix stored start on 32-byte borders
+  int ld;              // columns between the rows of out and du (GLU_GRAD: of the scratch dg and du)
+  int wide, wide_h;    // rows of out and du, of h, start on 32-byte borders
   __nv_bfloat16* du;          // GLU_GRAD
   __nv_bfloat16* h;           // GLU_GRAD: h, or null
   const __nv_bfloat16* dh;    // GLU_GRAD
@@ -363,14 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row = (int64_t)(2 * t.m + rank) * half_rows + quarter * 32 + lane;
       const bool row_ok = row < rows && quarter * 32 + lane < half_rows;
       const int col0 = t.n * args.width + first * kStep;
-      const int64_t base = row * args.N + col0;
+      const int64_t base = row * args.ld + col0;
       // dh of this thread's row, loaded before the accumulator is ready
       [[maybe_unused]] uint4 dhq[MODE == GLU_GRAD ? 8 : 1];
       if constexpr (MODE == GLU_GRAD) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          dhq[q] = row_ok && q < 2 * count && col0 + 8 * q < args.N ? __ldg(reinterpret_cast<const uint4*>(args.dh + base) + q)
-                                                   : make_uint4(0u, 0u, 0u, 0u);
+          dhq[q] = row_ok && q < 2 * count && col0 + 8 * q < args.N
+                       ? __ldg(reinterpret_cast<const uint4*>(args.dh + row * args.N + col0) + q)
+                       : make_uint4(0u, 0u, 0u, 0u);
       }
       if (!wait_asleep(&tfull_bar[acc], acc_phase, &abort_s)) {
         abort_s = 1;
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             store16(out + at, o0, col, args.N, args.wide);
             if constexpr (MODE == GLU_GRAD) {
               store16(args.du + at, o1, col, args.N, args.wide);
-              if (args.h != nullptr) store16(args.h + at, o2, col, args.N, args.wide);
+              if (args.h != nullptr) store16(args.h + row * args.N + col, o2, col, args.N, args.wide_h);
             }
           }
         } else {
@@ -621,7 +623,7 @@ int64_t cut_wide(GluGemmArgs& w, int tiles_n) {
 }
 void plan_wide(int64_t N, int D, int H, GluGemmArgs& w) {
   w = GluGemmArgs{};
-  w.N = D;
+  w.N = w.ld = D;
   w.kb_half = tiles_of(H, BK);
   w.p[0] = product(N, 2 * w.kb_half, nullptr);
   w.p[1] = product(H, tiles_of(N, BK), nullptr);
@@ -638,7 +640,7 @@ int64_t part_floats(const GluProduct& p, int D) { return p.splits > 1 ? p.splits
 bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, int64_t N, int D, int H, Maps& m,
                 GluGemmArgs& a, int& pairs) {
   a = GluGemmArgs{};
-  a.N = H;
+  a.N = a.ld = H;
   a.p[0] = product(N, tiles_of(D, BK), out);
   const int room = num_sms() / 2;
   a.width = best_width(H, 128, 16, a.p[0].half_rows, [&](int tiles_n) {
@@ -683,12 +685,14 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
   a.du = static_cast<__nv_bfloat16*>(b.du);
   a.h = static_cast<__nv_bfloat16*>(b.h);
   a.dh = static_cast<const __nv_bfloat16*>(b.dh);
-  a.wide = H % 16 == 0 && on32(b.dg) && on32(b.du) && on32(b.h);
+  a.ld = glu_scratch_pitch(H);
+  a.wide = on32(b.dg) && on32(b.du);
+  a.wide_h = H % 16 == 0 && on32(b.h);
   cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, pairs, status, s)
                                     : launch_mode<GLU_GRAD, kActSilu>(m, a, pairs, status, s);
   if (e != cudaSuccess) return e;
   // dx = dg W_g + du W_u, dW_g = dgᵀ x, dW_u = duᵀ x
-  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)H * 2;
+  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)a.ld * 2;
   GluGemmArgs w;
   plan_wide(N, D, H, w);
   w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);

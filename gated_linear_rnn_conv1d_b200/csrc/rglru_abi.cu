@@ -941,13 +941,13 @@ bool valid_act8(int64_t N, int C) {
 bool valid_w4(int N, int K, int group) {
   return valid_R(N) && valid_R(K) && (group == 32 || group == 64 || group == 128) && K % group == 0;
 }
-// dg [N][H] | du [N][H] | x̂ [N][D] (from_act8), bf16 | partial sums of dx and dW, float32
+// dg, du [N][glu_scratch_pitch(H)] | x̂ [N][D] (from_act8), bf16 | partial sums of dx and dW, float32
 struct GluBwdLayout {
   size_t off_du, off_x, off_part, bytes;
 };
 GluBwdLayout glu_bwd_layout(int64_t N, int D, int H, bool from_act8) {
   GluBwdLayout L;
-  L.off_du = round256((size_t)N * H * 2);
+  L.off_du = round256((size_t)N * glu_scratch_pitch(H) * 2);
   L.off_x = 2 * L.off_du;
   L.off_part = L.off_x + (from_act8 ? round256((size_t)N * D * 2) : 0);
   L.bytes = L.off_part + round256(glu_backward_part_bytes(N, D, H));

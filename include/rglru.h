@@ -458,7 +458,7 @@ RGLRU_API int rglru_gemm_bf16(const void* A, const void* Bm, void* C, int64_t M,
  *   dh [N][H], dx [N][D], dW_gate and dW_up [H][D]: bf16, sums in float32
  *   h             [N][H] bf16 or NULL: the forward's h again, for the down projection's gradient
  *   workspace     at least rglru_glu_backward_workspace_bytes(N, D, H, 0) bytes, 256-byte aligned
- *                 (dg and du in bf16; where dx or dW is cut along its sum, the pieces in float32);
+ *                 (dg and du in bf16, their rows padded to 64 columns; where dx or dW is cut along its sum, the pieces in float32);
  *                 it needs no initialisation
  * rglru_glu_backward_act8: the same, x given as its 8-bit checkpoint (rglru_act8_pack): the
  *   gradients at x̂, which the tensor cores read without a further rounding. workspace: at least
