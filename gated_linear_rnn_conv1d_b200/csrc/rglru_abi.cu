@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
+#include <initializer_list>
 #include <mutex>
 #include <nvtx3/nvToolsExt.h>
 
@@ -373,7 +374,7 @@ const char* rglru_strerror(int status) {
   switch (status) {
     case RGLRU_OK: return "ok";
     case RGLRU_ERR_NULL: return "a required pointer is NULL";
-    case RGLRU_ERR_SHAPE: return "invalid shape (B, T >= 1; R, D >= 8 and multiples of 8; sizes in range)";
+    case RGLRU_ERR_SHAPE: return "invalid shape (B, T >= 1; R, D >= 8 and multiples of 8; sizes in range), or an output that overlaps another buffer";
     case RGLRU_ERR_ALIGN: return "a pointer is not 16-byte aligned (workspace: 256-byte)";
     case RGLRU_ERR_DTYPE: return "io_dtype not supported by this entry point";
     case RGLRU_ERR_WORKSPACE: return "workspace missing or too small";
@@ -935,8 +936,28 @@ bool valid_glu(int64_t N, int D, int H, int act) {
   return N >= 1 && N <= kMaxTokens && valid_R(D) && valid_R(H) && (act == kActGelu || act == kActSilu) &&
          ((N + 255) / 256) * (((D > H ? D : H) + 127) / 128) <= kMaxTokens;
 }
+size_t act8_scale_bytes(int64_t N, int C) { return (size_t)N * ((C + kAct8Group - 1) / kAct8Group); }
 bool valid_act8(int64_t N, int C) {
   return N >= 1 && N <= kMaxTokens && valid_R(C) && N * ((C + kAct8Group - 1) / kAct8Group) <= (int64_t)INT32_MAX * 64;
+}
+// What a call writes lies apart from what it reads and from what else it writes: tiles are written while others
+// are read.
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool apart(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && x < y + b.n && y < x + a.n;
+  };
+  for (const Span* w = writes.begin(); w != writes.end(); ++w) {
+    for (const Span* o = w + 1; o != writes.end(); ++o)
+      if (meet(*w, *o)) return false;
+    for (const Span& r : reads)
+      if (meet(*w, r)) return false;
+  }
+  return true;
 }
 bool valid_w4(int N, int K, int group) {
   return valid_R(N) && valid_R(K) && (group == 32 || group == 64 || group == 128) && K % group == 0;
@@ -967,6 +988,10 @@ int glu_backward_impl(const void* W_gate, const void* W_up, const void* x, const
   const GluBwdLayout L = glu_bwd_layout(N, D, H, from_act8);
   if (workspace == nullptr || workspace_bytes < L.bytes) return RGLRU_ERR_WORKSPACE;
   if (!aligned256(workspace)) return RGLRU_ERR_ALIGN;
+  const size_t weights = (size_t)H * D * 2, xs = (size_t)N * D * 2, hs = (size_t)N * H * 2;
+  if (!apart({{dx, xs}, {dW_gate, weights}, {dW_up, weights}, {h, hs}, {workspace, L.bytes}},
+             {{W_gate, weights}, {W_up, weights}, {x, xs}, {codes, xs / 2}, {scales, act8_scale_bytes(N, D)}, {dh, hs}}))
+    return RGLRU_ERR_SHAPE;
   int st = check_device();
   if (st != RGLRU_OK) return st;
   unsigned* status = global_status_word();
@@ -994,6 +1019,9 @@ int rglru_glu_forward(const void* W_gate, const void* W_up, const void* x, void*
   if (!valid_glu(N, D, H, activation)) return RGLRU_ERR_SHAPE;
   if (W_gate == nullptr || W_up == nullptr || x == nullptr || h == nullptr) return RGLRU_ERR_NULL;
   if (!aligned16(W_gate) || !aligned16(W_up) || !aligned16(x) || !aligned16(h)) return RGLRU_ERR_ALIGN;
+  const size_t weights = (size_t)H * D * 2;
+  if (!apart({{h, (size_t)N * H * 2}}, {{W_gate, weights}, {W_up, weights}, {x, (size_t)N * D * 2}}))
+    return RGLRU_ERR_SHAPE;
   int st = check_device();
   if (st != RGLRU_OK) return st;
   unsigned* status = global_status_word();
@@ -1031,6 +1059,8 @@ int rglru_act8_pack(const void* x, void* codes, void* scales, int64_t N, int C, 
   if (!valid_act8(N, C)) return RGLRU_ERR_SHAPE;
   if (x == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const size_t n = (size_t)N * C, xs = n * (io_dtype == RGLRU_BF16 ? 2 : 4);
+  if (!apart({{codes, n}, {scales, act8_scale_bytes(N, C)}}, {{x, xs}})) return RGLRU_ERR_SHAPE;
   const int st = check_device();
   if (st != RGLRU_OK) return st;
   const cudaError_t e = launch_act8_pack(x, codes, scales, N, C, io_dtype == RGLRU_BF16, (cudaStream_t)stream);
@@ -1044,6 +1074,8 @@ int rglru_act8_unpack(const void* codes, const void* scales, void* x, int64_t N,
   if (!valid_act8(N, C)) return RGLRU_ERR_SHAPE;
   if (x == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const size_t n = (size_t)N * C, xs = n * (io_dtype == RGLRU_BF16 ? 2 : 4);
+  if (!apart({{x, xs}}, {{codes, n}, {scales, act8_scale_bytes(N, C)}})) return RGLRU_ERR_SHAPE;
   const int st = check_device();
   if (st != RGLRU_OK) return st;
   const cudaError_t e = launch_act8_unpack(codes, scales, x, N, C, io_dtype == RGLRU_BF16, (cudaStream_t)stream);
@@ -1055,6 +1087,8 @@ int rglru_w4_quantize(const void* W, void* codes, void* scales, int N, int K, in
   if (!valid_w4(N, K, group)) return RGLRU_ERR_SHAPE;
   if (W == nullptr || codes == nullptr || scales == nullptr) return RGLRU_ERR_NULL;
   if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return RGLRU_ERR_ALIGN;
+  const size_t n = (size_t)N * K;
+  if (!apart({{codes, n / 2}, {scales, n / group * 2}}, {{W, 2 * n}})) return RGLRU_ERR_SHAPE;
   const int st = check_device();
   if (st != RGLRU_OK) return st;
   const cudaError_t e = launch_w4_quantize(W, codes, scales, N, K, group, (cudaStream_t)stream);
@@ -1067,6 +1101,9 @@ int rglru_w4_linear(const void* codes, const void* scales, const void* x, void* 
   if (!valid_w4(N, K, group) || M < 1 || M > kW4MaxTokens) return RGLRU_ERR_SHAPE;
   if (codes == nullptr || scales == nullptr || x == nullptr || y == nullptr) return RGLRU_ERR_NULL;
   if (!aligned16(codes) || !aligned16(scales) || !aligned16(x) || !aligned16(y)) return RGLRU_ERR_ALIGN;
+  const size_t n = (size_t)N * K;
+  if (!apart({{y, (size_t)M * N * 2}}, {{codes, n / 2}, {scales, n / group * 2}, {x, (size_t)M * K * 2}}))
+    return RGLRU_ERR_SHAPE;
   const int st = check_device();
   if (st != RGLRU_OK) return st;
   const cudaError_t e = launch_w4_linear({codes, scales}, x, y, M, N, K, group, (cudaStream_t)stream);
@@ -1084,6 +1121,10 @@ int rglru_w4_glu(const void* gate_codes, const void* gate_scales, const void* up
   if (!aligned16(gate_codes) || !aligned16(gate_scales) || !aligned16(up_codes) || !aligned16(up_scales) ||
       !aligned16(x) || !aligned16(h))
     return RGLRU_ERR_ALIGN;
+  const size_t n = (size_t)H * D;
+  if (!apart({{h, (size_t)M * H * 2}}, {{gate_codes, n / 2}, {gate_scales, n / group * 2}, {up_codes, n / 2},
+                                        {up_scales, n / group * 2}, {x, (size_t)M * D * 2}}))
+    return RGLRU_ERR_SHAPE;
   const int st = check_device();
   if (st != RGLRU_OK) return st;
   const cudaError_t e = launch_w4_glu({gate_codes, gate_scales}, {up_codes, up_scales}, x, h, M, H, D, group,

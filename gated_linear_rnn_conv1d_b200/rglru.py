@@ -651,8 +651,8 @@ def _new(x: torch.Tensor, shape, dtype: torch.dtype, stream: Optional[torch.cuda
         return x.new_empty(shape, dtype=dtype)
 
 
-def _reads(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
-    """Tells the caching allocator that a stream other than their own reads these tensors."""
+def _used_on(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
+    """Tells the caching allocator that a stream other than their own reads or writes these tensors."""
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
@@ -691,7 +691,7 @@ def glu_forward(W_gate: torch.Tensor, W_up: torch.Tensor, x: torch.Tensor, *, ac
                                  _current_stream(dev) if stream is None else stream.cuda_stream)
     if code:
         _abi.check("rglru_glu_forward", code)
-    _reads(stream, W_gate, W_up, x)
+    _used_on(stream, W_gate, W_up, x, h)
     return h
 
 
@@ -739,7 +739,7 @@ def act8_pack(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None) ->
                                _current_stream(dev) if stream is None else stream.cuda_stream)
     if code:
         _abi.check("rglru_act8_pack", code)
-    _reads(stream, x)
+    _used_on(stream, x)
     return Act8(codes, scales, x.dtype)
 
 
@@ -761,7 +761,7 @@ def act8_unpack(a: Act8, *, x: Optional[torch.Tensor] = None,
                                  _io(x), _current_stream(dev) if stream is None else stream.cuda_stream)
     if code:
         _abi.check("rglru_act8_unpack", code)
-    _reads(stream, a.codes, a.scales)
+    _used_on(stream, a.codes, a.scales, x)
     return x
 
 
@@ -808,11 +808,11 @@ def glu_backward(W_gate: torch.Tensor, W_up: torch.Tensor, x: Union[torch.Tensor
     if packed:
         _abi.check("rglru_glu_backward_act8", lib.rglru_glu_backward_act8(
             W_gate.data_ptr(), W_up.data_ptr(), x.codes.data_ptr(), x.scales.data_ptr(), *tail))
-        _reads(stream, W_gate, W_up, x.codes, x.scales, dh)
+        _used_on(stream, W_gate, W_up, x.codes, x.scales, dh, ws)
     else:
         _abi.check("rglru_glu_backward", lib.rglru_glu_backward(W_gate.data_ptr(), W_up.data_ptr(), x.data_ptr(),
                                                                 *tail))
-        _reads(stream, W_gate, W_up, x, dh)
+        _used_on(stream, W_gate, W_up, x, dh, ws)
     return out
 
 
@@ -854,7 +854,7 @@ def w4_quantize(W: torch.Tensor, group: int = 128, *, stream: Optional[torch.cud
     _abi.check("rglru_w4_quantize", lib.rglru_w4_quantize(
         W.data_ptr(), codes.data_ptr(), scales.data_ptr(), N, K, group,
         _current_stream(dev) if stream is None else stream.cuda_stream))
-    _reads(stream, W)
+    _used_on(stream, W)
     return W4Weight(codes, scales, group)
 
 
@@ -879,7 +879,7 @@ def w4_linear(w: W4Weight, x: torch.Tensor, *, y: Optional[torch.Tensor] = None,
                                _current_stream(dev) if stream is None else stream.cuda_stream)
     if code:
         _abi.check("rglru_w4_linear", code)
-    _reads(stream, w.codes, w.scales, x)
+    _used_on(stream, w.codes, w.scales, x, y)
     return y
 
 
@@ -908,7 +908,7 @@ def w4_glu(w_gate: W4Weight, w_up: W4Weight, x: torch.Tensor, *, activation: str
                             _current_stream(dev) if stream is None else stream.cuda_stream)
     if code:
         _abi.check("rglru_w4_glu", code)
-    _reads(stream, w_gate.codes, w_gate.scales, w_up.codes, w_up.scales, x)
+    _used_on(stream, w_gate.codes, w_gate.scales, w_up.codes, w_up.scales, x, h)
     return h
 
 

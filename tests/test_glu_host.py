@@ -27,8 +27,8 @@ def test_glu_forward_refusals():
 def test_glu_backward_refusals(packed):
     lib = _abi.load()
     need = lib.rglru_glu_backward_workspace_bytes(4, 64, 72, int(packed))
-    # dg and du, and x̂ for the packed form, each rounded up to 256 bytes
-    assert need == 2 * 768 + (512 if packed else 0)
+    # dg and du with rows of 128 columns, and x̂ for the packed form, each rounded up to 256 bytes
+    assert need == 2 * 1024 + (512 if packed else 0)
     assert lib.rglru_glu_backward_workspace_bytes(0, 64, 72, 0) == 0
     assert lib.rglru_glu_backward_workspace_bytes(4, 60, 72, 0) == 0
 
@@ -91,3 +91,51 @@ def test_binding_takes_cuda_tensors_only():
                  lambda: rglru.w4_glu(w4, w4, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_outputs_apart_from_inputs():
+    """A call whose output overlaps an input, another output or the workspace is refused; the last byte of one
+    and the first of the next are apart (the call then ends at the device check where there is no B200)."""
+    lib = _abi.load()
+    base = 1 << 32
+
+    def at(i):  # 4096 bytes each, room for any buffer of these shapes but the weights' 9216
+        return base + 16384 * i
+
+    refused = lambda code: code == -2
+    N, D, H = 4, 64, 72
+    sizes = {"wg": H * D * 2, "wu": H * D * 2, "x": N * D * 2, "h": N * H * 2}
+
+    def fwd(**over):
+        p = {k: at(i) for i, k in enumerate(("wg", "wu", "x", "h"))} | over
+        return lib.rglru_glu_forward(p["wg"], p["wu"], p["x"], p["h"], N, D, H, 0, None)
+
+    for i, k in enumerate(("wg", "wu", "x")):
+        assert refused(fwd(h=at(i))) and refused(fwd(h=at(i) + sizes[k] - 16)), k
+        assert refused(fwd(h=at(i) - sizes["h"] + 16)), k
+    if not torch.cuda.is_available():
+        assert not refused(fwd()) and not refused(fwd(wu=at(0)))
+        assert not refused(fwd(h=at(2) + sizes["x"])) and not refused(fwd(h=at(2) - sizes["h"]))
+
+    names = ("wg", "wu", "x", "dh", "dx", "dwg", "dwu", "h", "ws")
+    need = lib.rglru_glu_backward_workspace_bytes(N, D, H, 0)
+
+    def bwd(**over):
+        p = {k: at(i) for i, k in enumerate(names)} | over
+        return lib.rglru_glu_backward(*(p[k] for k in names[:8]), N, D, H, 0, p["ws"], need, None)
+
+    for out in ("dx", "dwg", "dwu", "h", "ws"):
+        for other in range(len(names)):
+            if names[other] != out:
+                assert refused(bwd(**{out: at(other)})), (out, names[other])
+    if not torch.cuda.is_available():
+        assert not refused(bwd()) and not refused(bwd(wu=at(0))) and not refused(bwd(h=None))
+
+    assert refused(lib.rglru_act8_pack(at(0), at(0), at(1), 3, 40, 0, None))
+    assert refused(lib.rglru_act8_pack(at(0), at(1), at(1) + 112, 3, 40, 0, None))
+    assert refused(lib.rglru_act8_unpack(at(0), at(1), at(1) - 224, 3, 40, 0, None))
+    assert refused(lib.rglru_w4_quantize(at(0), at(0) + 32, at(1), 8, 64, 32, None))
+    assert refused(lib.rglru_w4_linear(at(0), at(1), at(2), at(2), 2, 64, 64, 32, None))
+    assert refused(lib.rglru_w4_linear(at(0), at(1), at(2), at(1), 2, 64, 64, 32, None))
+    assert refused(lib.rglru_w4_glu(at(0), at(1), at(2), at(3), at(4), at(4), 2, 64, 64, 32, 0, None))
+    assert refused(lib.rglru_w4_glu(at(0), at(1), at(2), at(3), at(4), at(3), 2, 64, 64, 32, 0, None))

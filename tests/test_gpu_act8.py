@@ -78,6 +78,17 @@ def test_many_rows():
         assert torch.equal(rglru.act8_unpack(part), b[lo:lo + 500])
 
 
+@pytest.mark.parametrize("C", [65536, 65528])  # whole groups in a row, and a short one
+def test_offsets_past_32_bits(C):
+    few = _draw(8, C, BF, seed=4).to(DEV)
+    want = rglru.act8_pack(few)
+    a = rglru.act8_pack(few.repeat(5000, 1))
+    assert torch.equal(a.codes[-8:], want.codes) and torch.equal(a.scales[-8:], want.scales)
+    assert torch.equal(a.codes[:8], want.codes) and torch.equal(a.scales[:8], want.scales)
+    back = rglru.act8_unpack(a)
+    assert torch.equal(back[-8:], rglru.act8_unpack(want)) and torch.equal(back[:8], back[-8:])
+
+
 @pytest.mark.parametrize("N,D,H", [(1, 40, 72), (30, 264, 136), (300, 136, 520)])
 def test_training_step_through_a_checkpoint(N, D, H):
     """The operators as a layer uses them: forward, the checkpoint in the place of x, backward from it; bit for

@@ -1,5 +1,9 @@
 """The gated feed-forward block on the GPU, forward and backward, against the float64 oracle; the bounds are
 derived in _glu.py."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +16,7 @@ from _util import f64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = Path(__file__).resolve().parent.parent
 BF = torch.bfloat16
 
 
@@ -244,6 +249,8 @@ def test_binding_refusals():
         (ValueError, lambda: rglru.glu_backward(Wg, Wu, x, dh[:5].contiguous())),
         (ValueError, lambda: rglru.glu_backward(Wg, Wu, x, dh, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))),
         (rglru._abi.RGLRUError, lambda: rglru.glu_forward(Wg, Wu, x[:0])),
+        (rglru._abi.RGLRUError, lambda: rglru.glu_forward(x, x, x, h=x.view(-1)[:36].view(6, 6))),
+        (rglru._abi.RGLRUError, lambda: rglru.glu_forward(Wg[:64], Wu[:64], x, h=x)),
         (rglru._abi.RGLRUError, lambda: rglru.glu_forward(Wg[:, :60].contiguous(), Wu[:, :60].contiguous(),
                                                           x[:, :60].contiguous())),
     ]
@@ -251,3 +258,83 @@ def test_binding_refusals():
         with pytest.raises(err):
             call()
             raise AssertionError(f"case {i} was taken")
+
+
+def test_weights_from_the_call_before():
+    """A call's weights are the output of the call before, in the same memory every time: what the kernel may fetch
+    before that call has ended must not be what it reads."""
+    x, Wg, Wu, _ = (t.to(DEV) for t in _draw(16, 264, 1032, seed=2))
+    z = [_draw(n, 1032, 8, seed=n)[0].to(DEV) for n in (4, 40)]
+    W = torch.empty(16, 1032, dtype=BF, device=DEV)
+    xs = [(x * (1 + i / 8)).to(BF) for i in range(12)]
+    want = []
+    for t in xs:
+        rglru.glu_forward(Wg, Wu, t, h=W)
+        torch.cuda.synchronize()
+        want.append([rglru.glu_forward(W, W, v) for v in z])
+        torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for t in xs:
+            rglru.glu_forward(Wg, Wu, t, h=W)
+            got.append([rglru.glu_forward(W, W, v) for v in z])
+        assert all(torch.equal(g, w) for a, b in zip(got, want) for g, w in zip(a, b))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in h, and bytes in a weight: the last rows are what the same rows give alone."""
+    N, D, H = 40000, 16, 65536
+    x, Wg, Wu, _ = (t.to(DEV) for t in _draw(8, D, H))
+    tokens = x.repeat(N // 8, 1)
+    h = rglru.glu_forward(Wg, Wu, tokens)
+    small = rglru.glu_forward(Wg, Wu, tokens[:256].contiguous())
+    assert torch.equal(h[-256:], small)
+    _check_forward(x, Wg, Wu, "gelu", h[-8:])
+    # gradients reach the first and the last tokens only: dW is theirs
+    dh = torch.zeros(N, H, dtype=BF, device=DEV)
+    g = torch.randn(8, H, generator=torch.Generator("cpu").manual_seed(5)).to(BF).to(DEV)
+    dh[:4], dh[-4:] = g[:4], g[4:]
+    got = rglru.glu_backward(Wg, Wu, tokens, dh)
+    assert rglru.workspace_status(None) == 0
+    assert (got["dx"][4:-4] == 0).all()
+    got = {"dx": torch.cat([got["dx"][:4], got["dx"][-4:]]), "dW_gate": got["dW_gate"], "dW_up": got["dW_up"], "h": None}
+    _check_backward(x, Wg, Wu, g, "gelu", got)
+    del h, dh, tokens
+    # the streaming kernel: 65536 rows of 32776 inputs, 4.3 GB a matrix
+    D = 32776
+    W = torch.randn(64, D, generator=torch.Generator("cpu").manual_seed(6)).div(D ** 0.5).to(BF).to(DEV)
+    Wg, Wu = W.repeat(1024, 1), W.roll(1, 0).repeat(1024, 1)
+    z = torch.randn(3, D, generator=torch.Generator("cpu").manual_seed(7)).to(BF).to(DEV)
+    h = rglru.glu_forward(Wg, Wu, z).view(3, 1024, 64)
+    assert torch.equal(h, rglru.glu_forward(W, W.roll(1, 0), z).unsqueeze(1).expand_as(h))
+
+
+FIRST = """
+import sys, torch
+from gated_linear_rnn_conv1d_b200 import rglru
+BF = torch.bfloat16
+r = lambda *s: torch.randn(*s, device="cuda", dtype=BF)
+Wg, Wu, x, few, dh = r(136, 64), r(136, 64), r(70, 64), r(3, 64), r(70, 136)
+w = rglru.W4Weight(torch.zeros(136, 32, dtype=torch.uint8, device="cuda"), r(136, 2), 32)
+torch.cuda.synchronize()
+def work():
+    a = rglru.act8_pack(x)
+    return [rglru.glu_forward(Wg, Wu, few), rglru.glu_forward(Wg, Wu, x), *rglru.glu_backward(Wg, Wu, x, dh).values(),
+            a.codes, rglru.act8_unpack(a), rglru.glu_backward(Wg, Wu, a, dh)["dx"], rglru.w4_linear(w, few),
+            rglru.w4_glu(w, w, few), rglru.w4_quantize(Wg, 32).codes]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = work()
+graph.replay()
+torch.cuda.synchronize()
+want = work()
+torch.cuda.synchronize()
+assert all(g is None or torch.equal(g, v) for g, v in zip(got, want))
+print("captured")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """Nothing that a first call sets up stands in the way of a capture."""
+    out = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr
