@@ -70,7 +70,7 @@ def _build_calls(force: bool) -> None:
            os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
     cmd = ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden"]
     cmd += [f"-I{d}" for d in inc] + [src, "-o", CALLS, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
-                                      "-lc10", "-lc10_cuda", "-L" + PKG, "-l:librglru.so", "-Wl,-rpath,$ORIGIN"]
+                                      "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:librglru.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")

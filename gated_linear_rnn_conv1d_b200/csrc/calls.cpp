@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -32,10 +33,15 @@ bool same_lead(at::IntArrayRef a, at::IntArrayRef b) {
   return a.size() == b.size() && a.slice(0, a.size() - 1).equals(b.slice(0, b.size() - 1));
 }
 
+// Uninitialised memory from the caching allocator, for the current stream. (Asked for directly: the way through the
+// dispatcher takes 0.3 µs more, of calls that take 3.5 with one allocation.)
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int device) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)device), std::nullopt));
+}
 at::Tensor with_last(const at::Tensor& x, int64_t last, at::ScalarType type) {
   c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
   shape.back() = last;
-  return at::empty(shape, x.options().dtype(type).requires_grad(false));
+  return fresh(shape, type, x.get_device());
 }
 
 // `out` as given (None: a new tensor) for a result of x's leading shape and `last` columns; undefined if it does
@@ -126,9 +132,8 @@ PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t N = x->numel() / D;
     const size_t bytes = rglru_glu_backward_workspace_bytes(N, (int)D, (int)H, packed);
     if (bytes == 0) return nullptr;
-    at::Tensor dx = with_last(*x, D, at::kBFloat16), dwg = at::empty({H, D}, wg->options().requires_grad(false)),
-               dwu = at::empty({H, D}, wg->options().requires_grad(false)), h,
-               ws = at::empty({(int64_t)bytes}, x->options().dtype(at::kByte).requires_grad(false));
+    at::Tensor dx = with_last(*x, D, at::kBFloat16), dwg = fresh({H, D}, at::kBFloat16, d),
+               dwu = fresh({H, D}, at::kBFloat16, d), h, ws = fresh({(int64_t)bytes}, at::kByte, d);
     if (want_h) h = with_last(*x, H, at::kBFloat16);
     void* hp = want_h ? h.mutable_data_ptr() : nullptr;
     rglru_stream_t s = stream_of(d);

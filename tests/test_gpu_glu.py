@@ -309,6 +309,21 @@ def test_offsets_past_32_bits():
     assert torch.equal(h, rglru.glu_forward(W, W.roll(1, 0), z).unsqueeze(1).expand_as(h))
 
 
+def test_outputs_as_torch_makes_them():
+    """On the inputs' device, outside autograd, inference tensors where torch's own would be."""
+    x, Wg, Wu, dh = (t.to(DEV) for t in _draw(5, 64, 72))
+    calls = lambda: [rglru.glu_forward(Wg, Wu, x), *rglru.glu_backward(Wg, Wu, x, dh, want_h=True).values(),
+                     rglru.act8_pack(x).codes, rglru.act8_unpack(rglru.act8_pack(x))]
+    want = calls()
+    Wg.requires_grad_(), x.requires_grad_()
+    plain = calls()
+    with torch.inference_mode():
+        inside = calls()
+    for a, b, c in zip(want, plain, inside):
+        assert torch.equal(a, b) and torch.equal(a, c) and a.device == x.device
+        assert not (a.requires_grad or b.requires_grad or a.is_inference()) and c.is_inference()
+
+
 FIRST = """
 import sys, torch
 from gated_linear_rnn_conv1d_b200 import rglru
