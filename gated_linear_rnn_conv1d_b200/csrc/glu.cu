@@ -31,11 +31,10 @@ constexpr int BK = 64;  // 64 bf16 = one 128-byte swizzle row
 constexpr int kMaxStages = 16;
 constexpr int kABytes = 128 * BK * 2;  // this CTA's 128 rows of A
 constexpr int kBBytes = 128 * BK * 2;  // this CTA's half of the B tile
-// The ring: as many stages as fit, each of the rows that are loaded (seven of the largest; few tokens and
-// narrow tiles have up to 16: the bytes in flight are what HBM's latency asks for. Of weights that are not in
-// L2, D 4096, H 12288, 64 tokens take 51.3 µs and 57.3 with six stages of the largest; 256 tokens 57.3 and
-// 61.3; from 2048 tokens on there is no difference). An MMA reads 128 rows of A whatever was loaded: up
-// to kABytes from a stage's start have to be there.
+// The ring has as many stages as fit, of the rows that are loaded (set_ring): the bytes in flight are what HBM's
+// latency asks for. Of weights that are not in L2, D 4096, H 12288, 64 tokens take 51.3 µs and 57.3 with six
+// stages of the largest; 256 tokens 57.3 and 61.3; from 2048 tokens on there is no difference. An MMA reads 128
+// rows of A whatever was loaded: up to kABytes from a k-block's start have to be there.
 constexpr int kRingBytes = 7 * (kABytes + kBBytes);
 constexpr int kSmem = kRingBytes + 1024;
 constexpr int kTmemCols = 512;  // two 256-column accumulators
@@ -54,6 +53,8 @@ struct GluProduct {
   int64_t M;             // output rows
   int tiles_m, half_rows;
   int k_blocks;
+  // a stage of the ring: `group` k-blocks of kb_bytes each, B's rows b_at from a k-block's start
+  int group, b_at, kb_bytes;
   __nv_bfloat16* out;
   // k may be cut into `splits` pieces of kb_per k-blocks, each a tile of its own that writes its float32 sums
   // to part [splits][M][N]; a second kernel adds them, in order
@@ -63,7 +64,7 @@ struct GluProduct {
 
 struct GluGemmArgs {
   int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
-  int stages, stage_bytes, b_at;  // the ring; B's place in a stage
+  int stages, stage_bytes;  // the ring
   int tiles_n, width;  // of every product; width: channels (up to 128), or columns (up to 256)
   int ld;              // columns between the rows of out and du (GLU_GRAD: of the scratch dg and du)
   int wide, wide_h;    // rows of out and du, of h, start on 32-byte borders
@@ -165,7 +166,8 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, vola
   }
 }
 
-template <int MODE, int ACT>
+// GROUP: 1 where every stage has one k-block
+template <int MODE, int ACT, int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -247,24 +249,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int half_rows = t.which == 0 ? args.p[0].half_rows : 128;
       const int arow = (2 * t.m + (int)rank) * half_rows;
       const uint32_t bytes = 2 * (half_rows * BK * 2 + b_bytes);
+      const GluProduct& p = kGated || t.which == 0 ? args.p[0] : args.p[1];
+      const int group = GROUP == 1 ? 1 : p.group, b_at = p.b_at, kb_bytes = p.kb_bytes;
       const int bcol = kGated ? t.n * args.width : t.n * args.width + (int)rank * half_cols;
       const bool is_dx = kGated || t.which == 0;
       const bool second = !kGated && t.which == 2;
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+      for (int kb = t.kb0; kb < t.kb1; kb += group) {
         ok = __all_sync(0xffffffffu, wait_asleep(&empty_bar[stage], phase ^ 1, &abort_s));
         if (!ok) break;
-        uint8_t* sa = smem + stage * args.stage_bytes;
-        uint8_t* sb = sa + args.b_at;
+        uint8_t* stage_at = smem + stage * args.stage_bytes;
         const uint32_t lbar = leader_full0 + stage * 8;
-        if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], bytes);
+        const int n = GROUP == 1 ? 1 : min(group, t.kb1 - kb);
+        const uint32_t stage_tx = n * bytes;
+        auto load = [&](int k, uint8_t* sa) {  // (by one lane)
+          uint8_t* sb = sa + b_at;
           if constexpr (kGated) {
-            tma_load_2d_2sm(sa, &tmA0, lbar, kb * BK, arow);
-            tma_load_2d_2sm(sb, leader ? &tmB0 : &tmB1, lbar, kb * BK, bcol);
+            tma_load_2d_2sm(sa, &tmA0, lbar, k * BK, arow);
+            tma_load_2d_2sm(sb, leader ? &tmB0 : &tmB1, lbar, k * BK, bcol);
           } else {
             // an MN-major operand: 128 columns as two boxes of 64 columns × BK rows
-            const bool du = kb >= args.kb_half;
-            const int kc = (is_dx && du ? kb - args.kb_half : kb) * BK;
+            const bool du = k >= args.kb_half;
+            const int kc = (is_dx && du ? k - args.kb_half : k) * BK;
             const CUtensorMap* mb = is_dx ? (du ? &tmB1 : &tmB0) : &tmX;
             if (is_dx) {
               tma_load_2d_2sm(sa, du ? &tmA1 : &tmA0, lbar, kc, arow);
@@ -275,6 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_2sm(sb, mb, lbar, bcol, kc);
             if (two) tma_load_2d_2sm(sb + kBBytes / 2, mb, lbar, bcol + 64, kc);
           }
+        };
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_tx);
+          load(kb, stage_at);
+          if constexpr (GROUP > 1)
+            for (int i = 1; i < n; ++i) load(kb + i, stage_at + i * kb_bytes);
         }
         __syncwarp();
         if (++stage == args.stages) { stage = 0; phase ^= 1; }
@@ -298,31 +309,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const GluProduct& p = kGated || t.which == 0 ? args.p[0] : args.p[1];
+        const int group = GROUP == 1 ? 1 : p.group, b_at = p.b_at, kb_bytes = p.kb_bytes;
+        for (int kb = t.kb0; kb < t.kb1; kb += group) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, &abort_s));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem0 + stage * args.stage_bytes;
-          const uint32_t b_addr = a_addr + args.b_at;
+          const uint32_t stage_at = smem0 + stage * args.stage_bytes;
+          const uint32_t first = kb == t.kb0 ? 0u : 1u;
           // one MMA takes 16 of k: 32 bytes along K-major rows, 16 rows of 128 B of an MN-major box (in
           // units of 16 bytes, the descriptors' start address)
-          const uint32_t first = kb == t.kb0 ? 0u : 1u;
-          const uint64_t a_k = umma_desc_sw128(a_addr), b_k = umma_desc_sw128(b_addr);
-          const uint64_t a_m = umma_desc_sw128_mn(a_addr, kABytes / 2), b_m = umma_desc_sw128_mn(b_addr, kBBytes / 2);
-          if (elect_one()) {
+          struct Block {
+            uint64_t a_k, b_k, a_m, b_m;
+          };
+          auto block = [&](uint32_t a_addr) {
+            const uint32_t b_addr = a_addr + b_at;
+            return Block{umma_desc_sw128(a_addr), umma_desc_sw128(b_addr), umma_desc_sw128_mn(a_addr, kABytes / 2),
+                         umma_desc_sw128_mn(b_addr, kBBytes / 2)};
+          };
+          auto issue = [&](const Block& d, uint32_t first) {  // (by one lane)
             if (kGated) {
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                umma_f16_2sm(d_tmem, a_k + k * 2, b_k + k * 2, idesc, k == 0 ? first : 1u);
+                umma_f16_2sm(d_tmem, d.a_k + k * 2, d.b_k + k * 2, idesc, k == 0 ? first : 1u);
             } else if (a_mn) {
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                umma_f16_2sm(d_tmem, a_m + k * 128, b_m + k * 128, idesc | kIdescAMN | kIdescBMN, k == 0 ? first : 1u);
+                umma_f16_2sm(d_tmem, d.a_m + k * 128, d.b_m + k * 128, idesc | kIdescAMN | kIdescBMN, k == 0 ? first : 1u);
             } else {
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                umma_f16_2sm(d_tmem, a_k + k * 2, b_m + k * 128, idesc | kIdescBMN, k == 0 ? first : 1u);
+                umma_f16_2sm(d_tmem, d.a_k + k * 2, d.b_m + k * 128, idesc | kIdescBMN, k == 0 ? first : 1u);
             }
+          };
+          const Block b0 = block(stage_at);
+          if (elect_one()) {
+            issue(b0, first);
+            if constexpr (GROUP > 1)
+              for (int i = 1; i < min(group, t.kb1 - kb); ++i) issue(block(stage_at + i * kb_bytes), 1u);
             umma_commit_2sm_both(&empty_bar[stage]);
           }
           __syncwarp();
@@ -506,9 +530,9 @@ struct Maps {
   CUtensorMap a0, a1, b0, b1, c0, c1, x;
 };
 
-template <int MODE, int ACT>
-cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
-  auto kern = glu_gemm_kernel<MODE, ACT>;
+template <int MODE, int ACT, int GROUP>
+cudaError_t launch_group(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
+  auto kern = glu_gemm_kernel<MODE, ACT, GROUP>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -536,6 +560,12 @@ cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsig
   return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, args, status);
 }
 
+template <int MODE, int ACT>
+cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
+  return args.p[0].group == 1 && (MODE != GLU_WIDE || args.p[1].group == 1) ? launch_group<MODE, ACT, 1>(m, args, pairs, status, s)
+                              : launch_group<MODE, ACT, 2>(m, args, pairs, status, s);
+}
+
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
 bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
@@ -544,12 +574,26 @@ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 // which 2.1 are the stores).
 int tile_cost(int k_blocks) { return std::max(k_blocks + 2, 12); }
 
-// The ring for stages of a_rows rows of A and b_bytes of B (multiples of 1024 bytes).
-void set_ring(GluGemmArgs& g, int a_rows, int b_bytes) {
-  g.b_at = a_rows * BK * 2;
-  g.stage_bytes = g.b_at + b_bytes;
-  // (the last stage's A is read to kABytes from its start)
-  g.stages = std::min(kMaxStages, (kRingBytes - std::max(0, kABytes - g.stage_bytes)) / g.stage_bytes);
+// The ring. A product's k-block has half_rows of A and b_bytes of B (multiples of 1024 bytes). Handing a stage over
+// costs the issuing warp 0.12 µs and its MMAs 0.10 µs a k-block for 32 channels (0.14 for 64, 0.28 for 128): with
+// narrow tiles a stage has up to four k-blocks, as long as five stages fit (four of dx's and dW's). D 4096, H 2048:
+// 64 tokens 29 → 16.7 µs, 256 tokens 18.5 → 14.6; D 256, H 768, 64 tokens backward 13.2 → 9.9. Tiles of 128 channels
+// keep one: their MMAs hide the handing over, and the loop over a stage's k-blocks, which one lane runs, costs
+// them 4 % (hence two kernels).
+void set_ring(GluGemmArgs& g, int products, int b_bytes) {
+  int reach = 0;  // an MMA reads kABytes from a k-block's start whatever was loaded
+  int most = products == 1 ? (kRingBytes - kABytes) / 5 : kRingBytes / 4;
+  g.stage_bytes = 0;
+  for (int i = products - 1; i >= 0; --i) {
+    GluProduct& p = g.p[i];
+    p.b_at = p.half_rows * BK * 2;
+    p.kb_bytes = p.b_at + b_bytes;
+    p.group = std::max(1, std::min(4, most / p.kb_bytes));
+    g.stage_bytes = std::max(g.stage_bytes, p.group * p.kb_bytes);
+    most = g.stage_bytes;  // (dx's k-blocks fit dW's stages)
+    reach = std::max(reach, (p.group - 1) * p.kb_bytes + std::max(kABytes, p.kb_bytes));
+  }
+  g.stages = std::min(kMaxStages, (kRingBytes - std::max(0, reach - g.stage_bytes)) / g.stage_bytes);
 }
 
 // Deals out n_long tiles of `a` k-blocks and n_short of `b` ≤ a to `pairs` CTA pairs (GluGemmArgs); returns the
@@ -587,7 +631,14 @@ template <class F> int best_width(int cols, int most, int step, int half_rows, F
 
 GluProduct product(int64_t rows, int k_blocks, void* out) {
   const int tiles = tiles_of(rows, 256);
-  return {rows, tiles, 8 * tiles_of(rows, 16 * tiles), k_blocks, static_cast<__nv_bfloat16*>(out), 1, k_blocks, nullptr};
+  GluProduct p{};
+  p.M = rows;
+  p.tiles_m = tiles;
+  p.half_rows = 8 * tiles_of(rows, 16 * tiles);
+  p.k_blocks = p.kb_per = k_blocks;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.splits = 1;
+  return p;
 }
 
 // dx, dW_g and dW_u: the tile width, and in how many pieces of k they are formed. A product whose k-blocks are
@@ -631,7 +682,7 @@ void plan_wide(int64_t N, int D, int H, GluGemmArgs& w) {
   w.p[2] = w.p[1];
   w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)cut_wide(w, tiles_n); });
   w.tiles_n = tiles_of(D, w.width);
-  set_ring(w, 128, w.width > 128 ? kBBytes : kBBytes / 2);
+  set_ring(w, 3, w.width > 128 ? kBBytes : kBBytes / 2);
   cut_wide(w, w.tiles_n);
 }
 int64_t part_floats(const GluProduct& p, int D) { return p.splits > 1 ? p.splits * p.M * D : 0; }
@@ -647,7 +698,7 @@ bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, 
     return (double)deal((int64_t)a.p[0].tiles_m * tiles_n, a.p[0].k_blocks, 0, 0, room, a);
   });
   a.tiles_n = tiles_of(H, a.width);
-  set_ring(a, a.p[0].half_rows, a.width * BK * 2);
+  set_ring(a, 1, a.width * BK * 2);
   const int64_t tiles = (int64_t)a.p[0].tiles_m * a.tiles_n;
   if (tiles > INT32_MAX / 2) return false;
   pairs = (int)std::min<int64_t>(tiles, room);
