@@ -206,7 +206,7 @@ template <int NT, int MT, int SEG, int STEP, int RING, int GROUPS> struct FewCfg
   static constexpr int kSumBufs = MT * NT <= 2 ? 2 : 1;
   static constexpr int kScaleWords = GROUPS > 0 ? 8 * MT * kFewPanelPitch : 0;
   static constexpr int kSmem = kRingBytes + (kSumBufs * kSumFloats + kScaleWords) * 4;
-  static constexpr int kBlocks = NT <= 2 ? 2 : 1;  // per SM
+  static constexpr int kBlocks = NT <= 2 || GROUPS == 0 ? 2 : 1;  // per SM (32 tokens' sums and x take 255 registers)
   static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F
 
   // A panel's scales of a chunk's rows: warp w takes rows w and w + 8 of each granule, along the rows.
   constexpr int kGroups = F::template kGroups<SEG>;
-  constexpr int kPanelSegs = kGroups > 0 ? kFewPanel / (kGroups > 0 ? kGroups : 1) : 1;
+  constexpr int kPanelSegs = kGroups > 0 ? kFewPanel / (kGroups > 0 ? kGroups : 1) : kFewWarps;
   uint32_t* scales = reinterpret_cast<uint32_t*>(sums + Cfg::kSumBufs * Cfg::kSumFloats);
   struct Scales {
     unsigned short a[MT][kFewPanel / 32], b[MT][kFewPanel / 32];
@@ -373,14 +373,17 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
     for (int i = 0; i < turns; ++i) {
-      if (kGroups > 0 && i % (kPanelSegs / kFewWarps) == 0) {
-        if (i > 0 || chunk > 0) {
-          if (i > 0) __syncthreads();  // the last panel has been read (the last chunk's: behind its sums' barrier)
-          Scales v;
-          fetch_scales(v, gr, mt, i / (kPanelSegs / kFewWarps));
-          put_scales(v, mt);
+      if constexpr (kGroups > 0) {
+        constexpr int kPanelTurns = kPanelSegs / kFewWarps;
+        if (i % kPanelTurns == 0) {
+          if (i > 0 || chunk > 0) {
+            if (i > 0) __syncthreads();  // the last panel has been read (the last chunk's: behind its sums' barrier)
+            Scales v;
+            fetch_scales(v, gr, mt, i / kPanelTurns);
+            put_scales(v, mt);
+          }
+          __syncthreads();
         }
-        __syncthreads();
       }
       if (i >= my_segs) break;  // (only in the last turn, past its barriers)
       const int seg = warp + i * kFewWarps;

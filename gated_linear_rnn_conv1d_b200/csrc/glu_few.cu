@@ -1,5 +1,5 @@
 // The gated feed-forward block's forward for a few tokens (serving): h = act(x W_gᵀ) ⊙ (x W_uᵀ) with
-// x [N][D], N ≤ 16, bf16 weights streamed once by few_tokens.cuh's kernel.
+// x [N][D], N ≤ 32, bf16 weights streamed once by few_tokens.cuh's kernel.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -8,12 +8,18 @@
 
 namespace rglru {
 namespace {
-// The copies are three or four steps of one granule ahead. 201 MB of weights, eight tokens: chunks of 1, 2, 3 and 6
-// granules 34.2, 32.4, 32.0 and 33.0 µs (a chunk shares the loads of x, which are read through what shared
-// memory leaves of the L1); sixteen: 33.3 and 33.8 µs for 2 and 3.
+// The copies are two to four granules ahead. 201 MB of weights, eight tokens: chunks of 1, 2, 3 and 6 granules 34.2,
+// 32.4, 32.0 and 33.0 µs (a chunk shares the loads of x, which are read through what shared memory leaves of
+// the L1); sixteen: 33.3 and 33.8 for 2 and 3; 24: 38.2 and 37.9; 32, in steps of two granules and of one: 38.0 and
+// 43.5 (three granules a block, 6144 channels of 2048, in one chunk: 11.7 and 13.4). The tiles of 256 rows (glu.cu) take
+// 42 µs for 17 tokens to 64; of 34 MB, D 4096, H 2048, they take 16 and this 9 for 24 tokens and 10 for 32.
 template <int ACT> cudaError_t launch_act(const FewArgs& a, cudaStream_t s) {
-  return a.M <= 8 ? launch_few<FewBf16, true, ACT, 1, 3, 128, 1, 5>(a, s)
-                  : launch_few<FewBf16, true, ACT, 2, 2, 128, 1, 4>(a, s);
+  const int n = (a.rows / 8 + 2 * num_sms() - 1) / (2 * num_sms());  // granules of a block
+  return a.M <= 8    ? launch_few<FewBf16, true, ACT, 1, 3, 128, 1, 5>(a, s)
+         : a.M <= 16 ? launch_few<FewBf16, true, ACT, 2, 2, 128, 1, 4>(a, s)
+         : a.M <= 24 ? launch_few<FewBf16, true, ACT, 3, 3, 128, 1, 3>(a, s)
+         : n == 3    ? launch_few<FewBf16, true, ACT, 4, 3, 128, 1, 3>(a, s)
+                     : launch_few<FewBf16, true, ACT, 4, 2, 128, 2, 2>(a, s);
 }
 }  // namespace
 

@@ -217,7 +217,7 @@ cudaError_t launch_backward(const BwdArgs& g, const BwdLayout& L, void* ws, cuda
 cudaError_t launch_glu_forward(const void* W_gate, const void* W_up, const void* x, void* h, int64_t N, int D, int H,
                                int act, unsigned* status, cudaStream_t s);
 // the same for N ≤ kGluFewTokens, by the kernel that streams the weights past a few tokens
-constexpr int kGluFewTokens = 16;
+constexpr int kGluFewTokens = 32;
 cudaError_t launch_glu_few(const void* W_gate, const void* W_up, const void* x, void* h, int N, int D, int H, int act,
                            cudaStream_t s);
 // dg and du have rows of whole 128-byte lines: N = 1999, D = 1032, H = 2888, whose rows would else start 16 bytes

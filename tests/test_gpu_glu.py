@@ -66,7 +66,7 @@ def _check_backward(x, Wg, Wu, dh, act, got):
 # one token; one over a vector, a tile and a pair of tiles; widths below, at and past the tiles' 64,
 # 128 and 256; several tiles a CTA pair (9 × 21 tiles on 74 pairs)
 SHAPES = [(1, 8, 8), (1, 264, 776), (2, 72, 136), (3, 512, 128), (5, 1032, 264), (8, 256, 1000), (9, 136, 72),
-          (16, 264, 520), (17, 64, 264), (33, 520, 136), (64, 128, 256), (65, 264, 264), (129, 72, 520),
+          (16, 264, 520), (17, 64, 264), (23, 520, 136), (32, 1032, 392), (33, 520, 136), (64, 128, 256), (65, 264, 264), (129, 72, 520),
           (256, 264, 136), (257, 328, 392), (513, 136, 264), (2100, 72, 2600)]
 
 
@@ -81,8 +81,10 @@ def test_forward(N, D, H, act):
     _check_forward(x, Wg, Wu, act, h)
 
 
-# one token to sixteen: the channels of a block of the streaming kernel are two, four and nine granules of eight
-@pytest.mark.parametrize("N,D,H", [(1, 72, 4744), (8, 200, 9480), (3, 136, 20008), (9, 72, 4744), (16, 328, 20008)])
+# one token to 32: the channels of a block of the streaming kernel are two, four and nine granules of eight
+@pytest.mark.parametrize("N,D,H", [(1, 72, 4744), (8, 200, 9480), (3, 136, 20008), (9, 72, 4744), (16, 328, 20008), (17, 136, 9480),
+                                   (24, 264, 4744), (25, 72, 20008), (27, 136, 5000),
+                                   (32, 520, 9480)])
 def test_few_tokens_of_many_channels(N, D, H):
     x, Wg, Wu, _ = _draw(N, D, H, seed=N)
     h, untouched = _guarded((N, H))
