@@ -1,5 +1,5 @@
 // Products of a few tokens (M ≤ 64) with weight matrices: y = x Wᵀ, or the gated pair
-// h = act(x W_gᵀ) ⊙ (x W_uᵀ). What bounds them is the weights' way from HBM, each byte read once, so
+// h = act(x W_gᵀ) ⊙ (x W_uᵀ), forward or with what its backward makes of g and u. What bounds them is the weights' way from HBM, each byte read once, so
 // the kernel is a stream of weights with the products on the side:
 //
 // * 16 weight rows are a granule: in the gated form those of 8 channels, the gate's in rows 0–7 and the up
@@ -39,10 +39,13 @@ struct FewArgs {
   const __nv_bfloat16* scales0;  // 4-bit weights: [rows][K / G]
   const __nv_bfloat16* scales1;
   const __nv_bfloat16* x;        // [M][K]
-  __nv_bfloat16* out;            // [M][rows]
+  __nv_bfloat16* out;            // [M][rows], out_ld columns apart
+  const __nv_bfloat16* dh;       // the gated form's backward: [M][rows]; out and du are dg and du
+  __nv_bfloat16* du;
+  __nv_bfloat16* h;              // [M][rows], or null
   int64_t row_bytes;             // a multiple of 16
   int row_groups;                // K / G, or 0
-  int M, rows, K, granules;
+  int M, rows, K, granules, out_ld;
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool real) {
@@ -210,7 +213,7 @@ template <int NT, int MT, int SEG, int STEP, int RING, int GROUPS> struct FewCfg
   static_assert(kBlocks * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int STEP, int RING>
+template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int STEP, int RING, bool GRAD>
 __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F::template kGroups<SEG>>::kBlocks)
     few_kernel(FewArgs a) {
   using Cfg = FewCfg<NT, MT, SEG, STEP, RING, F::template kGroups<SEG>>;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F
   const int segs = (int)((a.row_bytes + SEG - 1) / SEG);
   // a block's tokens
   a.x += (int64_t)blockIdx.y * (8 * NT) * a.K;
-  a.out += (int64_t)blockIdx.y * (8 * NT) * a.rows;
+  a.out += (int64_t)blockIdx.y * (8 * NT) * a.out_ld;
   a.M = min(a.M - (int)blockIdx.y * (8 * NT), 8 * NT);
   const int turns = (segs + kFewWarps - 1) / kFewWarps;
   const int my_segs = segs > warp ? (segs - warp + kFewWarps - 1) / kFewWarps : 0;
@@ -435,24 +438,33 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += p[w * MT * NT * 4 * 32];
+      const int token = 8 * j + 2 * (lane % 4) + c % 2, col = (gr + m) * kGran + 8 * (c / 2) + lane / 4;
+      [[maybe_unused]] float u = 0.0f, slope;
       if constexpr (GLU) {
-        float u = 0.0f, none;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) u += p[w * MT * NT * 4 * 32 + 64];
-        v = v * act_gate<ACT, false>(v, none) * u;
       }
-      const int token = 8 * j + 2 * (lane % 4) + c % 2, col = (gr + m) * kGran + 8 * (c / 2) + lane / 4;
-      if (token < a.M && col < a.rows) a.out[(int64_t)token * a.rows + col] = __float2bfloat16_rn(v);
+      if (token >= a.M || col >= a.rows) continue;
+      const int64_t at = (int64_t)token * a.out_ld + col;
+      if constexpr (GRAD) {  // (roundings as the tiles': glu.cu)
+        const float d = __bfloat162float(a.dh[(int64_t)token * a.rows + col]), act = v * act_gate<ACT, true>(v, slope);
+        a.out[at] = __float2bfloat16_rn(d * u * slope);
+        a.du[at] = __float2bfloat16_rn(d * act);
+        if (a.h != nullptr) a.h[(int64_t)token * a.rows + col] = __float2bfloat16_rn(act * u);
+      } else {
+        if constexpr (GLU) v = v * act_gate<ACT, false>(v, slope) * u;
+        a.out[at] = __float2bfloat16_rn(v);
+      }
     }
     if (Cfg::kSumBufs == 2) buf ^= 1;
   }
   cp_async_wait<0>();
 }
 
-template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int STEP, int RING>
+template <class F, bool GLU, int ACT, int NT, int MT, int SEG, int STEP, int RING, bool GRAD = false>
 cudaError_t launch_few(FewArgs a, cudaStream_t s) {
   using Cfg = FewCfg<NT, MT, SEG, STEP, RING, F::template kGroups<SEG>>;
-  auto kern = few_kernel<F, GLU, ACT, NT, MT, SEG, STEP, RING>;
+  auto kern = few_kernel<F, GLU, ACT, NT, MT, SEG, STEP, RING, GRAD>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -12,6 +12,7 @@
 //   GLU_FWD   h: rank 0 stages 128 rows of W_g, rank 1 the same 128 rows of W_u, so a tile holds
 //             g in columns 0–127 and u of the same channels in 128–255.
 //   GLU_GRAD  the same products; the epilogue reads dh and writes dg, du (and h when asked for).
+//             (Up to kGluFewTokens tokens glu_few.cu does what these two do.)
 //   GLU_WIDE  dx, dW_g and dW_u in one launch: [dg | du]·[W_g; W_u] with the weights read in place as
 //             an MN-major operand, k over dg's channels and then over du's; dgᵀx and duᵀx with both
 //             operands MN-major in place, k over the tokens.
@@ -730,20 +731,25 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
   const int D = b.D, H = b.H;
   // dg, du (and h) from x, the weights and dh
   Maps m;
-  GluGemmArgs a;
   int pairs;
-  if (!gated_args(b.W_gate, b.W_up, b.x, b.dg, N, D, H, m, a, pairs)) return cudaErrorInvalidValue;
-  a.du = static_cast<__nv_bfloat16*>(b.du);
-  a.h = static_cast<__nv_bfloat16*>(b.h);
-  a.dh = static_cast<const __nv_bfloat16*>(b.dh);
-  a.ld = glu_scratch_pitch(H);
-  a.wide = on32(b.dg) && on32(b.du);
-  a.wide_h = H % 16 == 0 && on32(b.h);
-  cudaError_t e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, pairs, status, s)
-                                    : launch_mode<GLU_GRAD, kActSilu>(m, a, pairs, status, s);
+  cudaError_t e;
+  if (N <= kGluFewTokens) {
+    e = launch_glu_few_grad(b, s);
+  } else {
+    GluGemmArgs a;
+    if (!gated_args(b.W_gate, b.W_up, b.x, b.dg, N, D, H, m, a, pairs)) return cudaErrorInvalidValue;
+    a.du = static_cast<__nv_bfloat16*>(b.du);
+    a.h = static_cast<__nv_bfloat16*>(b.h);
+    a.dh = static_cast<const __nv_bfloat16*>(b.dh);
+    a.ld = glu_scratch_pitch(H);
+    a.wide = on32(b.dg) && on32(b.du);
+    a.wide_h = H % 16 == 0 && on32(b.h);
+    e = b.act == kActGelu ? launch_mode<GLU_GRAD, kActGelu>(m, a, pairs, status, s)
+                          : launch_mode<GLU_GRAD, kActSilu>(m, a, pairs, status, s);
+  }
   if (e != cudaSuccess) return e;
   // dx = dg W_g + du W_u, dW_g = dgᵀ x, dW_u = duᵀ x
-  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)a.ld * 2;
+  const uint64_t rowD = (uint64_t)D * 2, rowH = (uint64_t)glu_scratch_pitch(H) * 2;
   GluGemmArgs w;
   plan_wide(N, D, H, w);
   w.wide = D % 16 == 0 && on32(b.dx) && on32(b.dW_gate) && on32(b.dW_up);

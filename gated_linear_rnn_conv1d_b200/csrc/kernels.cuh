@@ -240,6 +240,8 @@ struct GluBwdArgs {
   int D, H, act;
 };
 cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStream_t s);
+// dg, du and h for N ≤ kGluFewTokens
+cudaError_t launch_glu_few_grad(const GluBwdArgs& b, cudaStream_t s);
 size_t glu_backward_part_bytes(int64_t N, int D, int H);
 // x [rows][C] (bf16 or float32) ↔ int8 codes [rows][C] and scale bytes [rows][⌈C/32⌉]; C a
 // multiple of 8.

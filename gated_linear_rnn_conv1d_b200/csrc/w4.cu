@@ -54,6 +54,7 @@ FewArgs few_args(const W4Matrix& w0, const W4Matrix& w1, const void* x, void* ou
                  int group) {
   FewArgs a{};
   a.row_groups = K / group;
+  a.out_ld = rows;
   a.w0 = static_cast<const uint8_t*>(w0.codes);
   a.w1 = static_cast<const uint8_t*>(w1.codes);
   a.scales0 = static_cast<const __nv_bfloat16*>(w0.scales);
