@@ -38,9 +38,13 @@ constexpr int kBBytes = 128 * BK * 2;  // this CTA's half of the B tile
 // rows of A whatever was loaded: up to kABytes from a k-block's start have to be there.
 constexpr int kRingBytes = 7 * (kABytes + kBBytes);
 constexpr int kSmem = kRingBytes + 1024;
+// Tiles of dW whose k is short leave by TMA, from two boxes of 32 rows × 64 columns for each epilogue warp, behind a
+// smaller ring.
+constexpr int kBoxBytes = 32 * 64 * 2, kBoxes = 2;
 constexpr int kTmemCols = 512;  // two 256-column accumulators
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kAllBoxes = kEpiWarps * kBoxes * kBoxBytes;
 // Output tiles are taken in bands of kBand tile rows, column by column: the 74 pairs at work at
 // a time then cover about 8 × 9 tiles, whose operands (17 · 256 rows of k) stay in L2 between them.
 constexpr int kBand = 8;
@@ -66,6 +70,7 @@ struct GluProduct {
 struct GluGemmArgs {
   int N;               // output columns: H channels (GLU_FWD, GLU_GRAD) or D
   int stages, stage_bytes;  // the ring
+  int staged, least;        // dW leaves through shared memory; what a tile costs at least (tile_cost)
   int tiles_n, width;  // of every product; width: channels (up to 128), or columns (up to 256)
   int ld;              // columns between the rows of out and du (GLU_GRAD: of the scratch dg and du)
   int wide, wide_h;    // rows of out and du, of h, start on 32-byte borders
@@ -167,13 +172,14 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, vola
   }
 }
 
-// GROUP: 1 where every stage has one k-block
-template <int MODE, int ACT, int GROUP>
+// GROUP: 1 where every stage has one k-block. STAGED: dW's tiles leave through shared memory by TMA
+template <int MODE, int ACT, int GROUP, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                     const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-                    const __grid_constant__ CUtensorMap tmX, const GluGemmArgs args, unsigned* status) {
+                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmO1,
+                    const __grid_constant__ CUtensorMap tmO2, const GluGemmArgs args, unsigned* status) {
   // GLU_FWD, GLU_GRAD: A0 x, B0 W_g, B1 W_u. GLU_WIDE: A0 dg, A1 du, B0 W_g, B1 W_u (for dx); C0 dg, C1 du,
   // X x (for dW, in boxes of 64 columns).
   constexpr bool kGated = MODE != GLU_WIDE;
@@ -216,6 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmC0);
       tma_prefetch_desc(&tmC1);
       tma_prefetch_desc(&tmX);
+      if (STAGED) {
+        tma_prefetch_desc(&tmO1);
+        tma_prefetch_desc(&tmO2);
+      }
     }
   }
   if (warp == 1) {
@@ -381,6 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pieces = args.width / (kGated ? 16 : 32);
     const int first = half * ((pieces + 1) / 2), count = half == 0 ? (pieces + 1) / 2 : pieces / 2;
     constexpr int kStep = kGated ? 16 : 32;
+    [[maybe_unused]] int box_at = 0;  // STAGED: the box in use
+    [[maybe_unused]] uint8_t* const boxes = smem + kRingBytes - kAllBoxes + (warp - 2) * kBoxes * kBoxBytes;
     Tile t;
     for (int it = 0; tile_of<MODE>(args, it, cluster, n_clusters, t); ++it) {
       const int64_t rows = kGated || t.which == 0 ? args.p[0].M : args.p[1].M;
@@ -464,7 +476,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             o1[j] = __uint_as_float(rb[cur][j]);
           }
           float* part = t.which == 0 ? args.p[0].part : t.which == 1 ? args.p[1].part : args.p[2].part;
-          if (row_ok && part == nullptr) {
+          if (STAGED && t.which != 0) {
+            // a piece is half of a box: 64 of a row's 128 bytes, in 16-byte chunks permuted as the tensor map's
+            // swizzle has them (eight rows' chunks meet no bank twice)
+            uint8_t* box = boxes + box_at * kBoxBytes;
+            if ((k & 1) == 0) {
+              if (lane == 0) bulk_wait_read<kBoxes - 1>();  // the box's last store has been read (the others' may not)
+              __syncwarp();
+            }
+            const uint4 q[4] = {pack8(o0), pack8(o0 + 8), pack8(o1), pack8(o1 + 8)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(box + lane * 128 + (((k & 1) * 4 + c) ^ (lane & 7)) * 16) = q[c];
+            if ((k & 1) == 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int r0 = (2 * t.m + (int)rank) * 128 + quarter * 32, c0 = col - 32;
+                if (r0 < rows && c0 < args.N) tma_store_2d(t.which == 1 ? &tmO1 : &tmO2, box, c0, r0);
+                bulk_commit();
+              }
+              box_at = box_at + 1 == kBoxes ? 0 : box_at + 1;
+            }
+          } else if (row_ok && part == nullptr) {
             store16(out + at, o0, col, args.N, args.wide);
             store16(out + at + 16, o1, col + 16, args.N, args.wide);
           } else if (row_ok) {
@@ -483,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote(leader_tempty0 + acc * 8);
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
+    if (STAGED && lane == 0) bulk_wait();
   }
 
   tc_fence_before();
@@ -528,12 +563,12 @@ __global__ void __launch_bounds__(256) glu_sum_kernel(const GluSums a) {
 }
 
 struct Maps {
-  CUtensorMap a0, a1, b0, b1, c0, c1, x;
+  CUtensorMap a0, a1, b0, b1, c0, c1, x, o1, o2;
 };
 
-template <int MODE, int ACT, int GROUP>
+template <int MODE, int ACT, int GROUP, bool STAGED = false>
 cudaError_t launch_group(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
-  auto kern = glu_gemm_kernel<MODE, ACT, GROUP>;
+  auto kern = glu_gemm_kernel<MODE, ACT, GROUP, STAGED>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -558,22 +593,28 @@ cudaError_t launch_group(const Maps& m, const GluGemmArgs& args, int pairs, unsi
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, args, status);
+  return cudaLaunchKernelEx(&cfg, kern, m.a0, m.a1, m.b0, m.b1, m.c0, m.c1, m.x, m.o1, m.o2, args, status);
 }
 
 template <int MODE, int ACT>
 cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
-  return args.p[0].group == 1 && (MODE != GLU_WIDE || args.p[1].group == 1) ? launch_group<MODE, ACT, 1>(m, args, pairs, status, s)
-                              : launch_group<MODE, ACT, 2>(m, args, pairs, status, s);
+  const bool one = args.p[0].group == 1 && (MODE != GLU_WIDE || args.p[1].group == 1);
+  if constexpr (MODE == GLU_WIDE) {
+    if (args.staged)
+      return one ? launch_group<MODE, ACT, 1, true>(m, args, pairs, status, s)
+                 : launch_group<MODE, ACT, 2, true>(m, args, pairs, status, s);
+  }
+  return one ? launch_group<MODE, ACT, 1>(m, args, pairs, status, s) : launch_group<MODE, ACT, 2>(m, args, pairs, status, s);
 }
 
 int tiles_of(int64_t n, int t) { return (int)((n + t - 1) / t); }
 bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // What a tile of so many k-blocks costs in k-blocks (of about 0.3 µs): its accumulator changes hands, and
-// where its k is short the epilogue is what it takes (3.6 µs for 256 × 256 of dW with one k-block, of
-// which 2.1 are the stores).
-int tile_cost(int k_blocks) { return std::max(k_blocks + 2, 12); }
+// where its k is short the epilogue is what it takes: twelve for 256 × 256 of dW stored by the threads, each a row of
+// its own, eight where they leave by TMA (D 4096, H 12288: 16 tokens 153 → 139 µs, 64 tokens 157 → 144, 256 tokens
+// 172 → 162; D 2048, H 6144: 44.8 → 40.0, 48.0 → 43.9, 55.3 → 51.6).
+int tile_cost(int k_blocks, int least) { return std::max(k_blocks + 2, least); }
 
 // The ring. A product's k-block has half_rows of A and b_bytes of B (multiples of 1024 bytes). Handing a stage over
 // costs the issuing warp 0.12 µs and its MMAs 0.10 µs a k-block for 32 channels (0.14 for 64, 0.28 for 128): with
@@ -581,9 +622,9 @@ int tile_cost(int k_blocks) { return std::max(k_blocks + 2, 12); }
 // 64 tokens 29 → 16.7 µs, 256 tokens 18.5 → 14.6; D 256, H 768, 64 tokens backward 13.2 → 9.9. Tiles of 128 channels
 // keep one: their MMAs hide the handing over, and the loop over a stage's k-blocks, which one lane runs, costs
 // them 4 % (hence two kernels).
-void set_ring(GluGemmArgs& g, int products, int b_bytes) {
+void set_ring(GluGemmArgs& g, int products, int b_bytes, int ring) {
   int reach = 0;  // an MMA reads kABytes from a k-block's start whatever was loaded
-  int most = products == 1 ? (kRingBytes - kABytes) / 5 : kRingBytes / 4;
+  int most = products == 1 ? (ring - kABytes) / 5 : ring / 4;
   g.stage_bytes = 0;
   for (int i = products - 1; i >= 0; --i) {
     GluProduct& p = g.p[i];
@@ -594,7 +635,7 @@ void set_ring(GluGemmArgs& g, int products, int b_bytes) {
     most = g.stage_bytes;  // (dx's k-blocks fit dW's stages)
     reach = std::max(reach, (p.group - 1) * p.kb_bytes + std::max(kABytes, p.kb_bytes));
   }
-  g.stages = std::min(kMaxStages, (kRingBytes - std::max(0, reach - g.stage_bytes)) / g.stage_bytes);
+  g.stages = std::min(kMaxStages, (ring - std::max(0, reach - g.stage_bytes)) / g.stage_bytes);
 }
 
 // Deals out n_long tiles of `a` k-blocks and n_short of `b` ≤ a to `pairs` CTA pairs (GluGemmArgs); returns the
@@ -604,8 +645,8 @@ int64_t deal(int64_t n_long, int a, int64_t n_short, int b, int pairs, GluGemmAr
   g.n_short = (int)n_short;
   g.rest = (int)(n_long % pairs);
   const int others = pairs - g.rest;
-  a = tile_cost(a);
-  b = tile_cost(b);
+  a = tile_cost(a, g.least);
+  b = tile_cost(b, g.least);
   g.extra = g.rest == 0 || n_short == 0 ? 0 : (int)std::min<int64_t>(a / b, n_short / others);
   const int64_t turns = n_long / pairs, left = n_short - (int64_t)g.extra * others;
   const int64_t again = left / pairs, more = left % pairs;
@@ -657,7 +698,7 @@ int64_t share_wide(GluGemmArgs& w, int tiles_n, int pairs) {
 }
 int64_t cut_wide(GluGemmArgs& w, int tiles_n) {
   const int64_t n_dx = (int64_t)w.p[0].tiles_m * tiles_n, n_dw = 2 * (int64_t)w.p[1].tiles_m * tiles_n;
-  const int64_t all = n_dx * tile_cost(w.p[0].k_blocks) + n_dw * tile_cost(w.p[1].k_blocks);
+  const int64_t all = n_dx * tile_cost(w.p[0].k_blocks, w.least) + n_dw * tile_cost(w.p[1].k_blocks, w.least);
   const int64_t share = std::max<int64_t>(all / kPairs, 16);
   int64_t more = 0;
   for (int i = 0; i < 3; ++i) {
@@ -681,9 +722,13 @@ void plan_wide(int64_t N, int D, int H, GluGemmArgs& w) {
   w.p[1] = product(H, tiles_of(N, BK), nullptr);
   w.p[1].half_rows = 128;  // (read in boxes of 64 columns)
   w.p[2] = w.p[1];
-  w.width = best_width(D, 256, 32, 128, [&](int tiles_n) { return (double)cut_wide(w, tiles_n); });
+  // (below a tile a pair there is nothing to gain, D 256, H 768, 16 tokens 8.4 µs and staged 9.7; nor where rows are no
+  // whole lines, D 1032, H 2888, 100 tokens 25.0 and 26.9; nor from 512 tokens on, D 2048, H 6144 71.2 and 71.6)
+  w.staged = w.p[1].k_blocks <= 6 && D % 64 == 0 && 2 * w.p[1].tiles_m * tiles_of(D, 256) >= kPairs;
+  w.least = w.staged ? 8 : 12;
+  w.width = best_width(D, 256, w.staged ? 128 : 32, 128, [&](int tiles_n) { return (double)cut_wide(w, tiles_n); });
   w.tiles_n = tiles_of(D, w.width);
-  set_ring(w, 3, w.width > 128 ? kBBytes : kBBytes / 2);
+  set_ring(w, 3, w.width > 128 ? kBBytes : kBBytes / 2, kRingBytes - (w.staged ? kAllBoxes : 0));
   cut_wide(w, w.tiles_n);
 }
 int64_t part_floats(const GluProduct& p, int D) { return p.splits > 1 ? p.splits * p.M * D : 0; }
@@ -693,13 +738,14 @@ bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, 
                 GluGemmArgs& a, int& pairs) {
   a = GluGemmArgs{};
   a.N = a.ld = H;
+  a.least = 12;
   a.p[0] = product(N, tiles_of(D, BK), out);
   const int room = num_sms() / 2;
   a.width = best_width(H, 128, 16, a.p[0].half_rows, [&](int tiles_n) {
     return (double)deal((int64_t)a.p[0].tiles_m * tiles_n, a.p[0].k_blocks, 0, 0, room, a);
   });
   a.tiles_n = tiles_of(H, a.width);
-  set_ring(a, 1, a.width * BK * 2);
+  set_ring(a, 1, a.width * BK * 2, kRingBytes);
   const int64_t tiles = (int64_t)a.p[0].tiles_m * a.tiles_n;
   if (tiles > INT32_MAX / 2) return false;
   pairs = (int)std::min<int64_t>(tiles, room);
@@ -708,7 +754,7 @@ bool gated_args(const void* W_gate, const void* W_up, const void* x, void* out, 
   if (!make_map_2d(&m.a0, x, D, N, row, BK, a.p[0].half_rows) || !make_map_2d(&m.b0, W_gate, D, H, row, BK, a.width) ||
       !make_map_2d(&m.b1, W_up, D, H, row, BK, a.width))
     return false;
-  m.a1 = m.c0 = m.c1 = m.x = m.a0;  // (not read)
+  m.a1 = m.c0 = m.c1 = m.x = m.o1 = m.o2 = m.a0;  // (not read)
   return true;
 }
 
@@ -770,6 +816,8 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
       !make_map_2d(&m.b0, b.W_gate, D, H, rowD, 64, BK) || !make_map_2d(&m.b1, b.W_up, D, H, rowD, 64, BK) ||
       !make_map_2d(&m.c0, b.dg, H, N, rowH, 64, BK) || !make_map_2d(&m.c1, b.du, H, N, rowH, 64, BK) ||
       !make_map_2d(&m.x, b.x, D, N, rowD, 64, BK))
+    return cudaErrorInvalidValue;
+  if (w.staged && (!make_map_2d(&m.o1, b.dW_gate, D, H, rowD, 64, 32) || !make_map_2d(&m.o2, b.dW_up, D, H, rowD, 64, 32)))
     return cudaErrorInvalidValue;
   const int64_t tiles = ((int64_t)w.p[0].tiles_m * w.p[0].splits + 2 * (int64_t)w.p[1].tiles_m * w.p[1].splits) * w.tiles_n;
   if (tiles > INT32_MAX / 2 || (vectors + 255) / 256 > INT32_MAX) return cudaErrorInvalidValue;

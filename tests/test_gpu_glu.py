@@ -122,6 +122,25 @@ def test_backward_of_long_sums(N, D, H):
         assert all(torch.equal(again[k], got[k]) for k in got)
 
 
+# few tokens and large weights: where D is a multiple of 64 dW leaves in boxes of 32 × 64, which the last rows do not
+# fill, nor the last columns their tiles
+@pytest.mark.parametrize("N,D,H", [(40, 1088, 2600), (300, 2048, 1288), (17, 512, 4872), (384, 1344, 1800),
+                                   (100, 1032, 2600), (512, 1280, 1800)])
+def test_backward_of_large_weights(N, D, H):
+    x, Wg, Wu, dh = _draw(N, D, H, seed=N + 5)
+    ws = torch.full((rglru.glu_backward_workspace_bytes(N, D, H),), 0xFF, dtype=torch.uint8, device=DEV)
+    dev = [t.to(DEV) for t in (Wg, Wu, x, dh)]
+    out = {k: _guarded(s) for k, s in (("dx", (N, D)), ("dW_gate", (H, D)), ("dW_up", (H, D)), ("h", (N, H)))}
+    code = rglru._abi.load().rglru_glu_backward(
+        *(t.data_ptr() for t in dev), *(out[k][0].data_ptr() for k in out), N, D, H, 0, ws.data_ptr(), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    assert code == 0 and rglru.workspace_status(None) == 0
+    assert all(untouched() for _, untouched in out.values())
+    _check_backward(x, Wg, Wu, dh, "gelu", {k: v[0] for k, v in out.items()})
+    again = rglru.glu_backward(*dev, want_h=True)
+    assert all(torch.equal(again[k], out[k][0]) for k in out)
+
+
 def test_shapes_of_any_rank():
     x, Wg, Wu, dh = _draw(6, 40, 72)
     w = (Wg.to(DEV), Wu.to(DEV))
