@@ -153,6 +153,38 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16], 
   }
 }
 
+// The same for rows that may start in the middle of a sector (ODD kernels): such a row's second eight columns wait for
+// the next sixteen, so that its sectors too are stored whole, but for the first and the last (forward of 26090 tokens,
+// D 208, H 8952: 434 µs with stores of 16 bytes, 336 so; backward of one token, D 2072, H 5224: 45.7 and 40.3).
+struct RowStore {
+  uint4 held;
+  bool odd;
+  __device__ __forceinline__ explicit RowStore(const void* row)
+      : held(make_uint4(0u, 0u, 0u, 0u)), odd((reinterpret_cast<uintptr_t>(row) & 16u) != 0) {}
+  // columns col … col + 15; `first`: of the thread's
+  __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[16], int col, int cols, bool first) {
+    if (!odd) {
+      store16(p, v, col, cols, 1);
+      return;
+    }
+    const uint4 a = pack8(v), b = pack8(v + 8);
+    if (col >= cols) {
+      if (!first) flush(p, col, cols);
+    } else if (first) {
+      *reinterpret_cast<uint4*>(p) = a;
+    } else {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p - 8), "r"(held.x), "r"(held.y),
+                   "r"(held.z), "r"(held.w), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w)
+                   : "memory");
+    }
+    held = b;
+  }
+  // after the last: p, col are the next column's
+  __device__ __forceinline__ void flush(__nv_bfloat16* p, int col, int cols) const {
+    if (odd && col - 8 < cols) *reinterpret_cast<uint4*>(p - 8) = held;
+  }
+};
+
 // (part's rows are multiples of 32 bytes, as D is of eight)
 __device__ __forceinline__ void store8_f32(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -172,8 +204,9 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, vola
   }
 }
 
-// GROUP: 1 where every stage has one k-block. STAGED: dW's tiles leave through shared memory by TMA
-template <int MODE, int ACT, int GROUP, bool STAGED>
+// GROUP: 1 where every stage has one k-block. STAGED: dW's tiles leave through shared memory by TMA.
+// ODD: rows of out that may start off a sector's border
+template <int MODE, int ACT, int GROUP, bool STAGED, bool ODD>
 __global__ void __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -418,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256;
+      [[maybe_unused]] RowStore odd_row(out + base);
       // four pairs of 16 columns; the next pair's TMEM loads are in flight while one is worked on
       const uint32_t ta = t_row + first * kStep, tb = ta + (kGated ? args.width : 16);
       uint32_t ra[2][16], rb[2][16];
@@ -463,7 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (row_ok) {
-            store16(out + at, o0, col, args.N, args.wide);
+            if constexpr (ODD)
+              odd_row.put(out + at, o0, col, args.N, k == 0);
+            else
+              store16(out + at, o0, col, args.N, args.wide);
             if constexpr (MODE == GLU_GRAD) {
               store16(args.du + at, o1, col, args.N, args.wide);
               if (args.h != nullptr) store16(args.h + row * args.N + col, o2, col, args.N, args.wide_h);
@@ -499,8 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               box_at = box_at + 1 == kBoxes ? 0 : box_at + 1;
             }
           } else if (row_ok && part == nullptr) {
-            store16(out + at, o0, col, args.N, args.wide);
-            store16(out + at + 16, o1, col + 16, args.N, args.wide);
+            if constexpr (ODD) {
+              odd_row.put(out + at, o0, col, args.N, k == 0);
+              odd_row.put(out + at + 16, o1, col + 16, args.N, false);
+            } else {
+              store16(out + at, o0, col, args.N, args.wide);
+              store16(out + at + 16, o1, col + 16, args.N, args.wide);
+            }
           } else if (row_ok) {
             part += (int64_t)t.split * rows * args.N + at;
 #pragma unroll
@@ -511,6 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (k + 1 < count) tmem_ld_wait16(ra[cur ^ 1], rb[cur ^ 1]);
+      }
+      if constexpr (ODD) {
+        const float* part = kGated || t.which == 0 ? args.p[0].part : args.p[1].part;
+        if (row_ok && count > 0 && part == nullptr)
+          odd_row.flush(out + base + count * kStep, col0 + count * kStep, args.N);
       }
       tc_fence_before();
       __syncwarp();
@@ -566,9 +613,9 @@ struct Maps {
   CUtensorMap a0, a1, b0, b1, c0, c1, x, o1, o2;
 };
 
-template <int MODE, int ACT, int GROUP, bool STAGED = false>
+template <int MODE, int ACT, int GROUP, bool STAGED = false, bool ODD = false>
 cudaError_t launch_group(const Maps& m, const GluGemmArgs& args, int pairs, unsigned* status, cudaStream_t s) {
-  auto kern = glu_gemm_kernel<MODE, ACT, GROUP, STAGED>;
+  auto kern = glu_gemm_kernel<MODE, ACT, GROUP, STAGED, ODD>;
   static bool attr_set[64] = {};  // idempotent: a race sets it twice
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -603,6 +650,11 @@ cudaError_t launch_mode(const Maps& m, const GluGemmArgs& args, int pairs, unsig
     if (args.staged)
       return one ? launch_group<MODE, ACT, 1, true>(m, args, pairs, status, s)
                  : launch_group<MODE, ACT, 2, true>(m, args, pairs, status, s);
+  }
+  if constexpr (MODE != GLU_GRAD) {
+    if (!args.wide)
+      return one ? launch_group<MODE, ACT, 1, false, true>(m, args, pairs, status, s)
+                 : launch_group<MODE, ACT, 2, false, true>(m, args, pairs, status, s);
   }
   return one ? launch_group<MODE, ACT, 1>(m, args, pairs, status, s) : launch_group<MODE, ACT, 2>(m, args, pairs, status, s);
 }
@@ -776,7 +828,7 @@ cudaError_t launch_glu_backward(const GluBwdArgs& b, unsigned* status, cudaStrea
   const int64_t N = b.N;
   const int D = b.D, H = b.H;
   // dg, du (and h) from x, the weights and dh
-  Maps m;
+  Maps m{};
   int pairs;
   cudaError_t e;
   if (N <= kGluFewTokens) {
