@@ -335,7 +335,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == args.stages) { stage = 0; phase ^= 1; }
       }
     }
-    if (!ok && lane == 0) { abort_s = 1; atomicOr(status, kStatusTimeout); }
+    // What is under way to this CTA's shared memory arrives before the CTA may end: the last MMAs' arrivals on its
+    // empty barriers; and after a wait that ran out the copies themselves, which the leader's full barriers count for
+    // both CTAs.
+    for (int i = 0; ok && i < args.stages; ++i)
+      ok = __all_sync(0xffffffffu, wait_asleep(&empty_bar[i], i < stage ? phase : phase ^ 1, &abort_s));
+    if (!ok) {
+      if (lane == 0) { abort_s = 1; atomicOr(status, kStatusTimeout); }
+      volatile int never = 0;
+      bool there = leader;
+      for (int i = 0; there && i < args.stages; ++i)
+        there = __all_sync(0xffffffffu, mbar_wait(&full_bar[i], i < stage ? phase : phase ^ 1, &never));
+    }
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader CTA only) ----------------
     if (leader) {
