@@ -79,12 +79,13 @@ struct FewBf16 {
   static constexpr int kRead = 16;
   template <int SEG> static constexpr int kGroups = 0;
   static __device__ __forceinline__ int lane_k(int t) { return 8 * t; }
-  // x of a segment, as eight-value pieces; the lane's piece c is 32·c further
+  // x of a segment, as eight-value pieces; the lane's piece c is 32·c further. (x and the scales may be what the kernel
+  // ahead writes while this one already lives, which rules the non-coherent loads out.)
   template <int SEG> static constexpr int kX = SEG / 64;
   template <int SEG> static __device__ __forceinline__ uint4 load_x(const FewArgs& a, const __nv_bfloat16* xrow,
                                                                     int seg, int c, int lane) {
     const int k = seg * (SEG / 2) + c * 32;  // beyond K the weights are zeros; x is made so too
-    return k + 8 * (lane % 4) < a.K ? __ldg(reinterpret_cast<const uint4*>(xrow + k)) : make_uint4(0u, 0u, 0u, 0u);
+    return k + 8 * (lane % 4) < a.K ? *reinterpret_cast<const uint4*>(xrow + k) : make_uint4(0u, 0u, 0u, 0u);
   }
   // x of a segment in the products' order
   template <int NT, int N> static __device__ __forceinline__ void order(uint4 (&)[NT][N]) {}
@@ -141,7 +142,7 @@ template <int GROUP> struct FewW4 {
   template <int SEG> static __device__ __forceinline__ uint4 load_x(const FewArgs& a, const __nv_bfloat16* xrow,
                                                                     int seg, int c, int) {
     const int k = seg * (2 * SEG) + c / kWords * GROUP;
-    return k < a.K ? __ldg(reinterpret_cast<const uint4*>(xrow + k + 8 * (c % kWords))) : make_uint4(0u, 0u, 0u, 0u);
+    return k < a.K ? *reinterpret_cast<const uint4*>(xrow + k + 8 * (c % kWords)) : make_uint4(0u, 0u, 0u, 0u);
   }
   // x of a segment in the unpacked weights' order: pairs (k, k + 4)
   template <int NT, int N> static __device__ __forceinline__ void order(uint4 (&x)[NT][N]) {
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<NT, MT, SEG, STEP, RING, F
 #pragma unroll
       for (int g = 0; g < kFewPanel / 32; ++g) {
         const bool real = m < mt && g0 + 32 * g < a.row_groups;
-        v.a[m][g] = real ? __ldg(s0 + 32 * g) : 0;
-        v.b[m][g] = real ? __ldg(s1 + 32 * g) : 0;
+        v.a[m][g] = real ? s0[32 * g] : 0;
+        v.b[m][g] = real ? s1[32 * g] : 0;
       }
     }
   };

@@ -446,13 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = row < rows && quarter * 32 + lane < half_rows;
       const int col0 = t.n * args.width + first * kStep;
       const int64_t base = row * args.ld + col0;
-      // dh of this thread's row, loaded before the accumulator is ready
+      // dh of this thread's row, loaded before the accumulator is ready (coherently: it may be what the kernel ahead wrote
+      // while this one already lived)
       [[maybe_unused]] uint4 dhq[MODE == GLU_GRAD ? 8 : 1];
       if constexpr (MODE == GLU_GRAD) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           dhq[q] = row_ok && q < 2 * count && col0 + 8 * q < args.N
-                       ? __ldg(reinterpret_cast<const uint4*>(args.dh + row * args.N + col0) + q)
+                       ? reinterpret_cast<const uint4*>(args.dh + row * args.N + col0)[q]
                        : make_uint4(0u, 0u, 0u, 0u);
       }
       if (!wait_asleep(&tfull_bar[acc], acc_phase, &abort_s)) {

@@ -208,3 +208,34 @@ def test_binding_refusals():
         with pytest.raises(err):
             call()
             raise AssertionError(f"case {i} was taken")
+
+
+@pytest.mark.parametrize("M", [1, 8, 13, 32, 47])
+def test_inputs_from_the_call_before(M):
+    """The serving chain h = w4_glu(…), y = w4_linear(down, h): x is what the kernel ahead writes, in the same memory
+    every time, and so are scales and gradients; the results are those of calls that wait for each other."""
+    D, H, K = 640, 4744, 4736
+    wg, wu, down = _weight(H, D, 64, seed=1), _weight(H, D, 64, seed=2), _weight(D, K, 64, seed=3)
+    W = torch.randn(H, D, generator=torch.Generator("cpu").manual_seed(5)).to(BF).to(DEV)
+    xs = [(_x(M, D, seed=4) * (1 + i / 8)).to(BF).to(DEV) for i in range(12)]
+    h, y = torch.empty(M, H, dtype=BF, device=DEV), torch.empty(M, D, dtype=BF, device=DEV)
+
+    def chain(x, sync):
+        rglru.w4_glu(wg, wu, x, h=h)
+        sync()
+        rglru.w4_linear(down, h.view(-1)[:M * K].view(M, K), y=y)
+        sync()
+        few = rglru.glu_forward(W[:72], W[72:144], y)
+        sync()
+        dx = rglru.glu_backward(W[:72], W[72:144], y, few)["dx"]
+        sync()
+        q = rglru.w4_quantize((W * x.view(-1)[0]).contiguous(), 64)
+        sync()
+        last = rglru.w4_linear(q, dx)
+        sync()
+        return y.clone(), few, dx, last
+
+    want = [chain(x, torch.cuda.synchronize) for x in xs]
+    for _ in range(4):
+        got = [chain(x, lambda: None) for x in xs]
+        assert all(torch.equal(g, w) for a, b in zip(got, want) for g, w in zip(a, b))
