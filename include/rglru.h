@@ -484,11 +484,12 @@ RGLRU_API int rglru_glu_backward_act8(const void* W_gate, const void* W_up, cons
  * magnitude m is held as int8 codes and one power of two,
  *     e = the smallest integer ≥ −127 with |rint(x / 2^e)| ≤ 127,  code = rint(x / 2^e),
  *     x̂ = code · 2^e  (rint to even; |x̂ − x| ≤ 2^(e−1) ≤ m / 127 for m ≥ 2^-121).
- * x̂ is a bfloat16 number, so unpacking rounds nothing in either type. A group that holds an
- * infinity or a NaN comes back as NaN.
+ * From m = 127.5 · 2^121 on, where x̂ would be 2^128, e is 121 and codes are held within ±127
+ * (|x̂ − x| < 2^121 ≤ m / 127). x̂ is a finite bfloat16 number, so unpacking rounds nothing in either
+ * type. A group that holds an infinity or a NaN comes back as NaN.
  *   x       [N][C] io_dtype
  *   codes   [N][C] int8
- *   scales  [N][⌈C/32⌉] bytes: e + 127 (0 … 249), or 255 for a group that is not finite
+ *   scales  [N][⌈C/32⌉] bytes: e + 127 (0 … 248), or 255 for a group that is not finite
  * 1 ≤ N ≤ 2^30, C a multiple of 8 up to 65536.
  * --------------------------------------------------------------------------------- */
 RGLRU_API int rglru_act8_pack(const void* x, void* codes, void* scales, int64_t N, int C, int io_dtype,

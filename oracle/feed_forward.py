@@ -40,9 +40,10 @@ def glu_backward(x, W_gate, W_up, dh, name):
 
 
 def act8_pack(x):
-    """(codes [N][C] int64, exponents [N][⌈C/32⌉] int64 or None where the group is not finite, as a
-    masked array): for each group the smallest e ≥ −127 with |rint(x / 2^e)| ≤ 127, by trying
-    every exponent in turn."""
+    """(codes [N][C], scales [N][⌈C/32⌉], both int64): for each group the smallest −127 ≤ e ≤ 121 with
+    |rint(x / 2^e)| ≤ 127, by trying every exponent in turn, or 121 where none does, with the codes
+    held within ±127 (127 · 2^121 is the largest multiple that is a finite number of either type); the
+    scale is e + 127, or 255 where the group is not finite."""
     x = np.asarray(x, dtype=np.float64)
     N, C = x.shape
     groups = -(-C // 32)
@@ -55,9 +56,9 @@ def act8_pack(x):
                 scales[n, j] = 255
                 continue
             e = -127
-            while np.max(np.abs(np.rint(np.ldexp(v, -e)))) > 127:
+            while e < 121 and np.max(np.abs(np.rint(np.ldexp(v, -e)))) > 127:
                 e += 1
-            codes[n, 32 * j:32 * j + 32] = np.rint(np.ldexp(v, -e)).astype(np.int64)
+            codes[n, 32 * j:32 * j + 32] = np.clip(np.rint(np.ldexp(v, -e)), -127, 127).astype(np.int64)
             scales[n, j] = e + 127
     return codes, scales
 

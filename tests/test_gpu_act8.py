@@ -165,3 +165,42 @@ def test_binding_refusals():
         with pytest.raises(err):
             call()
             raise AssertionError(f"case {i} was taken")
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("C", [64, 72])
+def test_largest_numbers(C, dtype):
+    """The end of the type's range, where the next power of two is no finite number: every top from 126 · 2^121 on,
+    both signs, with smaller neighbours; codes, scales and x̂ as the oracle's, x̂ finite and within 1/127 of the top."""
+    info = torch.finfo(dtype)
+    tops = [126 * 2.0 ** 121, 126.5 * 2.0 ** 121, 127 * 2.0 ** 121, 127.5 * 2.0 ** 121, info.max, info.min]
+    if dtype is torch.float32:
+        tops += [127.25 * 2.0 ** 121, 127.5 * 2.0 ** 121 * (1 - 2.0 ** -24), 127.75 * 2.0 ** 121]
+    x = torch.zeros(2 * len(tops), C, dtype=torch.float64)
+    for i, t in enumerate(tops + [-t for t in tops]):
+        x[i, 3] = t
+        x[i, 32:64] = t * torch.arange(1, 33, dtype=torch.float64) / 32
+        x[i, 64:] = t / 2
+    x = x.to(dtype)
+    a = rglru.act8_pack(x.to(DEV))
+    _check(x, a)
+    back = rglru.act8_unpack(a)
+    assert torch.isfinite(back).all() and (a.codes >= -127).all()
+    m = torch.nn.functional.pad(f64t(x), (0, -C % 32)).view(len(x), -1, 32).abs().amax(2)
+    assert ((f64t(back) - f64t(x)).abs() <= m.repeat_interleave(32, 1)[:, :C] / 127).all()
+
+
+def test_backward_with_masked_channels_of_the_lowest_number():
+    """finfo.min in channels that no weight reads: the gradients from the checkpoint are finite, as those at x."""
+    N, D, H = 40, 72, 136
+    g = torch.Generator("cpu").manual_seed(8)
+    x = torch.randn(N, D, generator=g).to(BF)
+    x[:, 32:64] = torch.finfo(BF).min
+    Wg, Wu = ((torch.randn(H, D, generator=g) / D ** 0.5).to(BF) for _ in range(2))
+    Wg[:, 32:64], Wu[:, 32:64] = 0, 0
+    dh = torch.randn(N, H, generator=g).to(BF)
+    r = rglru.glu_backward(Wg.to(DEV), Wu.to(DEV), rglru.act8_pack(x.to(DEV)), dh.to(DEV), want_h=True)
+    keep = torch.ones(D, dtype=torch.bool)
+    keep[32:64] = False
+    assert torch.isfinite(r["dx"]).all() and torch.isfinite(r["h"]).all()
+    assert torch.isfinite(r["dW_gate"][:, keep]).all() and torch.isfinite(r["dW_up"][:, keep]).all()

@@ -81,3 +81,22 @@ def test_w4_order_and_scales():
     codes = np.array([[0x8F, 0x10] + [0x88] * 14], dtype=np.uint8)
     w = ff.w4_dequantize(codes, np.array([[0.5]]), 32)
     assert w[0, :4].tolist() == [0.5 * 7, 0.0, 0.5 * -8, 0.5 * -7] and not w[0, 4:].any()
+
+
+def test_act8_largest_numbers():
+    """127.5 · 2^121 and more would round up to 2^128: the exponent stays 121, the codes within ±127."""
+    top = 2.0 ** 121
+    x = np.zeros((1, 96))
+    x[0, 0], x[0, 1], x[0, 2] = 127.25 * top, -126.5 * top, 1.5 * top      # the last that need no care; 126 is even
+    x[0, 32], x[0, 33], x[0, 34] = -127.5 * top, 127.0 * top, 0.5 * top    # finfo(bfloat16).min
+    x[0, 64], x[0, 65] = float(torch.finfo(torch.float32).max), float(torch.finfo(torch.float32).min)
+    codes, scales = ff.act8_pack(x)
+    assert scales.tolist() == [[248, 248, 248]]
+    assert codes[0, :3].tolist() == [127, -126, 2]
+    assert codes[0, 32:35].tolist() == [-127, 127, 0]
+    assert codes[0, 64:66].tolist() == [127, -127]
+    back = ff.act8_unpack(codes, scales)
+    m = np.abs(x).reshape(1, 3, 32).max(2).repeat(32, axis=1)
+    assert (np.abs(back - x) <= m / 127).all()
+    assert torch.equal(torch.from_numpy(back).to(torch.bfloat16).double(), torch.from_numpy(back))
+    assert torch.isfinite(torch.from_numpy(back).to(torch.bfloat16)).all()
