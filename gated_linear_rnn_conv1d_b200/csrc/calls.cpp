@@ -69,12 +69,14 @@ PyObject* wrap(PyObject* out, at::Tensor t) {
   return THPVariable_Wrap(std::move(t));
 }
 
-// The library's call with the interpreter free for other threads, as ctypes leaves it.
+// The library's call with the interpreter free for other threads, as ctypes leaves it. Addresses and the stream are
+// asked for before it: that may throw (a tensor inside torch.func's transforms has no storage).
 template <class F> int call(F f) {
-  PyThreadState* state = PyEval_SaveThread();
-  const int r = f();
-  PyEval_RestoreThread(state);
-  return r;
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f();
 }
 
 // Runs f, which returns a new reference or null for "not this way"; C++ exceptions (out of memory among
@@ -82,7 +84,7 @@ template <class F> int call(F f) {
 template <class F> PyObject* guarded(F f) {
   try {
     if (PyObject* r = f()) return r;
-  } catch (const std::exception&) {
+  } catch (const std::exception&) {  // (none passes while the interpreter is released)
   }
   PyErr_Clear();
   Py_RETURN_NONE;
@@ -102,9 +104,11 @@ PyObject* glu_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long act = PyLong_AsLong(a[3]);
     at::Tensor h = result(a[4], *x, H, at::kBFloat16, d);
     if (!h.defined()) return nullptr;
-    if (call([&] { return rglru_glu_forward(wg->const_data_ptr(), wu->const_data_ptr(), x->const_data_ptr(), h.mutable_data_ptr(),
-                          x->numel() / D, (int)D, (int)H, (int)act, stream_of(d)); }) != RGLRU_OK)
-      return nullptr;
+    const void *wgp = wg->const_data_ptr(), *wup = wu->const_data_ptr(), *xp = x->const_data_ptr();
+    void* hp = h.mutable_data_ptr();
+    const int64_t N = x->numel() / D;
+    rglru_stream_t s = stream_of(d);
+    if (call([&] { return rglru_glu_forward(wgp, wup, xp, hp, N, (int)D, (int)H, (int)act, s); }) != RGLRU_OK) return nullptr;
     return wrap(a[4], std::move(h));
   });
 }
@@ -135,17 +139,14 @@ PyObject* glu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor dx = with_last(*x, D, at::kBFloat16), dwg = fresh({H, D}, at::kBFloat16, d),
                dwu = fresh({H, D}, at::kBFloat16, d), h, ws = fresh({(int64_t)bytes}, at::kByte, d);
     if (want_h) h = with_last(*x, H, at::kBFloat16);
-    void* hp = want_h ? h.mutable_data_ptr() : nullptr;
+    const void *wgp = wg->const_data_ptr(), *wup = wu->const_data_ptr(), *xp = x->const_data_ptr(),
+               *dhp = dh->const_data_ptr(), *scp = packed ? scales->const_data_ptr() : nullptr;
+    void *dxp = dx.mutable_data_ptr(), *dwgp = dwg.mutable_data_ptr(), *dwup = dwu.mutable_data_ptr(),
+         *wsp = ws.mutable_data_ptr(), *hp = want_h ? h.mutable_data_ptr() : nullptr;
     rglru_stream_t s = stream_of(d);
     const int r = call([&] {
-      return packed ? rglru_glu_backward_act8(wg->const_data_ptr(), wu->const_data_ptr(), x->const_data_ptr(),
-                                              scales->const_data_ptr(), dh->const_data_ptr(), dx.mutable_data_ptr(),
-                                              dwg.mutable_data_ptr(), dwu.mutable_data_ptr(), hp, N, (int)D, (int)H,
-                                              act, ws.mutable_data_ptr(), bytes, s)
-                    : rglru_glu_backward(wg->const_data_ptr(), wu->const_data_ptr(), x->const_data_ptr(),
-                                         dh->const_data_ptr(), dx.mutable_data_ptr(), dwg.mutable_data_ptr(),
-                                         dwu.mutable_data_ptr(), hp, N, (int)D, (int)H, act, ws.mutable_data_ptr(),
-                                         bytes, s);
+      return packed ? rglru_glu_backward_act8(wgp, wup, xp, scp, dhp, dxp, dwgp, dwup, hp, N, (int)D, (int)H, act, wsp, bytes, s)
+                    : rglru_glu_backward(wgp, wup, xp, dhp, dxp, dwgp, dwup, hp, N, (int)D, (int)H, act, wsp, bytes, s);
     });
     if (r != RGLRU_OK) return nullptr;
     PyObject* o[4] = {THPVariable_Wrap(std::move(dx)), THPVariable_Wrap(std::move(dwg)), THPVariable_Wrap(std::move(dwu)),
@@ -168,8 +169,11 @@ PyObject* act8_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t C = x->sizes().back();
     if (C < 1 || C > kWidest) return nullptr;
     at::Tensor codes = with_last(*x, C, at::kChar), scales = with_last(*x, (C + 31) / 32, at::kByte);
-    if (call([&] { return rglru_act8_pack(x->const_data_ptr(), codes.mutable_data_ptr(), scales.mutable_data_ptr(), x->numel() / C,
-                        (int)C, bf16 ? RGLRU_BF16 : RGLRU_F32, stream_of(d)); }) != RGLRU_OK)
+    const void* xp = x->const_data_ptr();
+    void *cp = codes.mutable_data_ptr(), *sp = scales.mutable_data_ptr();
+    const int64_t N = x->numel() / C;
+    rglru_stream_t st = stream_of(d);
+    if (call([&] { return rglru_act8_pack(xp, cp, sp, N, (int)C, bf16 ? RGLRU_BF16 : RGLRU_F32, st); }) != RGLRU_OK)
       return nullptr;
     PyObject* c = THPVariable_Wrap(std::move(codes));
     PyObject* s = THPVariable_Wrap(std::move(scales));
@@ -193,8 +197,11 @@ PyObject* act8_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool bf16 = a[2] == Py_True;
     at::Tensor x = result(a[3], *codes, C, bf16 ? at::kBFloat16 : at::kFloat, d);
     if (!x.defined()) return nullptr;
-    if (call([&] { return rglru_act8_unpack(codes->const_data_ptr(), scales->const_data_ptr(), x.mutable_data_ptr(), x.numel() / C,
-                          (int)C, bf16 ? RGLRU_BF16 : RGLRU_F32, stream_of(d)); }) != RGLRU_OK)
+    const void *cp = codes->const_data_ptr(), *sp = scales->const_data_ptr();
+    void* xp = x.mutable_data_ptr();
+    const int64_t N = x.numel() / C;
+    rglru_stream_t s = stream_of(d);
+    if (call([&] { return rglru_act8_unpack(cp, sp, xp, N, (int)C, bf16 ? RGLRU_BF16 : RGLRU_F32, s); }) != RGLRU_OK)
       return nullptr;
     return wrap(a[3], std::move(x));
   });
@@ -229,10 +236,11 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return nullptr;
     at::Tensor y = result(a[4], *x, w.N, at::kBFloat16, d);
     if (!y.defined()) return nullptr;
-    if (call([&] { return rglru_w4_linear(w.codes->const_data_ptr(), w.scales->const_data_ptr(), x->const_data_ptr(),
-                        y.mutable_data_ptr(), (int)(x->numel() / w.K), (int)w.N, (int)w.K, (int)group,
-                        stream_of(d)); }) != RGLRU_OK)
-      return nullptr;
+    const void *cp = w.codes->const_data_ptr(), *sp = w.scales->const_data_ptr(), *xp = x->const_data_ptr();
+    void* yp = y.mutable_data_ptr();
+    const int M = (int)(x->numel() / w.K);
+    rglru_stream_t s = stream_of(d);
+    if (call([&] { return rglru_w4_linear(cp, sp, xp, yp, M, (int)w.N, (int)w.K, (int)group, s); }) != RGLRU_OK) return nullptr;
     return wrap(a[4], std::move(y));
   });
 }
@@ -251,9 +259,12 @@ PyObject* w4_glu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long act = PyLong_AsLong(a[6]);
     at::Tensor h = result(a[7], *x, g.N, at::kBFloat16, d);
     if (!h.defined()) return nullptr;
-    if (call([&] { return rglru_w4_glu(g.codes->const_data_ptr(), g.scales->const_data_ptr(), u.codes->const_data_ptr(),
-                     u.scales->const_data_ptr(), x->const_data_ptr(), h.mutable_data_ptr(), (int)(x->numel() / g.K),
-                     (int)g.N, (int)g.K, (int)group, (int)act, stream_of(d)); }) != RGLRU_OK)
+    const void *gc = g.codes->const_data_ptr(), *gs = g.scales->const_data_ptr(), *uc = u.codes->const_data_ptr(),
+               *us = u.scales->const_data_ptr(), *xp = x->const_data_ptr();
+    void* hp = h.mutable_data_ptr();
+    const int M = (int)(x->numel() / g.K);
+    rglru_stream_t s = stream_of(d);
+    if (call([&] { return rglru_w4_glu(gc, gs, uc, us, xp, hp, M, (int)g.N, (int)g.K, (int)group, (int)act, s); }) != RGLRU_OK)
       return nullptr;
     return wrap(a[7], std::move(h));
   });

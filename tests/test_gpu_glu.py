@@ -374,3 +374,45 @@ def test_first_calls_may_be_captured():
     """Nothing that a first call sets up stands in the way of a capture."""
     out = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert out.returncode == 0 and "captured" in out.stdout, out.stdout + out.stderr
+
+
+TRANSFORMS = """
+import torch
+from gated_linear_rnn_conv1d_b200 import rglru
+BF = torch.bfloat16
+r = lambda *s: torch.randn(*s, device="cuda", dtype=BF)
+W, x, dh = r(72, 64), r(3, 64), r(3, 72)
+w4 = rglru.W4Weight(torch.zeros(72, 32, dtype=torch.uint8, device="cuda"), r(72, 1), 64)
+calls = {
+    "glu_forward": lambda v: rglru.glu_forward(W, W, v),
+    "glu_forward's weights": lambda v: rglru.glu_forward(v.expand(72, 64).contiguous() if v.dim() == 1 else v, W, x),
+    "glu_backward": lambda v: rglru.glu_backward(W, W, v, dh if v.dim() == 2 else dh[0]),
+    "act8_pack": rglru.act8_pack,
+    "act8_unpack": lambda v: rglru.act8_unpack(rglru.Act8(v.to(torch.int8), v[..., :2].to(torch.uint8), BF)),
+    "w4_quantize": lambda v: rglru.w4_quantize(v if v.dim() == 2 else v.expand(8, 64).contiguous(), 64),
+    "w4_linear": lambda v: rglru.w4_linear(w4, v),
+    "w4_glu": lambda v: rglru.w4_glu(w4, w4, v),
+}
+for name, call in calls.items():
+    def inside(v):
+        try:
+            call(v)
+        except (RuntimeError, ValueError, TypeError) as e:
+            seen.append(str(e))
+        return v.float().sum()
+    for run in (lambda: torch.vmap(inside)(x), lambda: torch.func.grad(inside)(x),
+                lambda: torch.func.jvp(inside, (x,), (x,))):
+        seen = []
+        run()
+        assert len(seen) == 1, name
+want = rglru.glu_forward(W, W, x)
+torch.cuda.synchronize()
+assert torch.isfinite(want).all()
+print("refused")
+"""
+
+
+def test_transforms_of_torch_func_are_refused():
+    """Inside vmap, grad and jvp a tensor has no memory to hand over: every operator raises an ordinary error."""
+    out = subprocess.run([sys.executable, "-c", TRANSFORMS], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert out.returncode == 0 and "refused" in out.stdout, out.stdout + out.stderr
