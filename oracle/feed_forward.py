@@ -10,7 +10,7 @@ from __future__ import annotations
 import math
 
 import numpy as np
-from scipy.special import erf, erfc
+from scipy.special import erfc
 
 
 def act(g, name):
@@ -23,7 +23,7 @@ def act(g, name):
 def act_slope(g, name):
     g = np.asarray(g, dtype=np.float64)
     if name == "gelu":
-        return 0.5 * (1.0 + erf(g / math.sqrt(2.0))) + g * np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+        return 0.5 * erfc(-g / math.sqrt(2.0)) + g * np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
     r = 1.0 / (1.0 + np.exp(-g))
     return r * (1.0 + g * (1.0 - r))
 

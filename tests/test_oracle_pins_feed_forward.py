@@ -100,3 +100,17 @@ def test_act8_largest_numbers():
     assert (np.abs(back - x) <= m / 127).all()
     assert torch.equal(torch.from_numpy(back).to(torch.bfloat16).double(), torch.from_numpy(back))
     assert torch.isfinite(torch.from_numpy(back).to(torch.bfloat16)).all()
+
+
+def test_gelu_slope_in_the_far_tail():
+    """Φ + gφ keeps its digits where Φ is far below one: against Φ's asymptotic series, whose terms alternate, so that
+    the error is below the first one left out."""
+    g = np.array([-8.0, -8.6875, -10.0, -13.0])
+    z = -g
+    phi = np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+    terms = [1.0]
+    for k in range(1, 12):
+        terms.append(-terms[-1] * (2 * k - 1) / z ** 2)
+    tail = phi / z * np.sum(np.broadcast_arrays(*terms[:-1]), axis=0)
+    want = tail + g * phi
+    assert (np.abs(ff.act_slope(g, "gelu") - want) <= phi / z * np.abs(terms[-1]) + 1e-12 * np.abs(want)).all()
