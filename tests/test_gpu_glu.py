@@ -11,7 +11,7 @@ import torch
 from gated_linear_rnn_conv1d_b200 import rglru
 from oracle import feed_forward as ff
 
-from _glu import backward_bounds, forward_bound
+from _glu import HALF, TINY, backward_bounds, forward_bound
 from _util import f64
 
 pytestmark = pytest.mark.gpu
@@ -416,3 +416,42 @@ def test_transforms_of_torch_func_are_refused():
     """Inside vmap, grad and jvp a tensor has no memory to hand over: every operator raises an ordinary error."""
     out = subprocess.run([sys.executable, "-c", TRANSFORMS], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert out.returncode == 0 and "refused" in out.stdout, out.stdout + out.stderr
+
+
+# What the kernels' activations may be off by, relative to their own size, for −13 ≤ g: GeLU's Φ(−|g|) is fitted to
+# 7.3e-5 of its value; z = g²/2·log₂e (g·log₂e for SiLU) is rounded twice, 2^-23 of up to 122, which is 1e-5 in the
+# exponential; the hardware's exponential and reciprocal add 2^-22 each and ten float32 operations 2^-24 each: 2e-4 with
+# room. The same holds for the two terms of the slope, whose sum may cancel. Below −13 the exponential is flushed.
+TAIL = 2e-4
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("N", [7, 32, 209])
+def test_tails_of_the_activation(N, act):
+    """g = x₀ and u = x₁ = 1 exactly, so that h is act(g) rounded once, dx₀ its slope and dx₁ act(g): each to half a step
+    of bf16 relative to its own value, however small that is."""
+    x = torch.zeros(N, 8)
+    x[:, 0] = torch.linspace(-13, 13, N)
+    x[:, 1] = 1
+    x = x.to(BF)
+    Wg, Wu = torch.zeros(8, 8, dtype=BF), torch.zeros(8, 8, dtype=BF)
+    Wg[0, 0], Wu[0, 1] = 1, 1
+    dh = torch.ones(N, 8, dtype=BF)
+    w = (Wg.to(DEV), Wu.to(DEV))
+    h = rglru.glu_forward(*w, x.to(DEV), activation=act)
+    r = rglru.glu_backward(*w, x.to(DEV), dh.to(DEV), activation=act, want_h=True)
+    g = f64(x)[:, 0]
+    a, s = ff.act(g, act), ff.act_slope(g, act)
+    gate = np.where(g == 0, 0.5, a / np.where(g == 0, 1.0, g))  # Φ or σ
+    terms = gate + np.abs(s - gate)
+
+    def check(what, got, ref, size):
+        e = TAIL * size
+        err, bound = np.abs(f64(got) - ref), e + HALF * (np.abs(ref) + e) + TINY
+        print(f"{what}: worst error / bound {np.max(err / bound):.3f} at g = {g[np.argmax(err / bound)]}")
+        assert (err <= bound).all(), what
+
+    check("h", h[:, 0], a, np.abs(a))
+    check("h again", r["h"][:, 0], a, np.abs(a))
+    check("du", r["dx"][:, 1], a, np.abs(a))
+    check("dg", r["dx"][:, 0], s, terms)
