@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "librglru.so")
@@ -142,6 +143,13 @@ def load() -> ctypes.CDLL:
 _calls = None
 
 
+class _NoCalls:
+    """In the place of _calls.so where it cannot be loaded: every call goes the binding's long way."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def calls():
     """The compiled short way to the calls of a few microseconds (csrc/calls.cpp)."""
     global _calls
@@ -150,8 +158,10 @@ def calls():
         try:
             from . import _calls as module
         except ImportError as e:
-            raise RuntimeError("_calls.so is missing or was built for another PyTorch: build it with "
-                               "`python -m gated_linear_rnn_conv1d_b200.build`") from e
+            warnings.warn(f"_calls.so is missing or was built for another PyTorch ({e}): calls of a few microseconds take "
+                          "some more. Build it with `python -m gated_linear_rnn_conv1d_b200.build`.", RuntimeWarning,
+                          stacklevel=3)
+            module = _NoCalls()
         _calls = module
     return _calls
 

@@ -4,7 +4,8 @@ way, csrc/calls.cpp) in-tree with nvcc and g++.
     python -m gated_linear_rnn_conv1d_b200.build [--force]
 
 Objects go to gated_linear_rnn_conv1d_b200/_build/, the libraries next to it. A source is recompiled when it or any
-header under csrc/ or include/ is newer than its object.
+header under csrc/ or include/ is newer than its object. librglru.so needs nvcc alone; where PyTorch or g++ is not
+there, _calls.so is left out.
 """
 from __future__ import annotations
 
@@ -59,7 +60,14 @@ def _compile(src: str, force: bool) -> str:
 
 
 def _build_calls(force: bool) -> None:
-    import torch
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    gxx = shutil.which("g++")
+    if torch is None or gxx is None:  # librglru.so needs neither, and the binding goes its long way without _calls.so
+        print(f"_calls.so is not built: {'PyTorch' if torch is None else 'g++'} not found", file=sys.stderr)
+        return
     src = os.path.join(CSRC, "calls.cpp")
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "rglru.h"), torch.version.__file__))
     if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
@@ -68,7 +76,7 @@ def _build_calls(force: bool) -> None:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(t, "include"),
            os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    cmd = ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden"]
+    cmd = [gxx, "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden"]
     cmd += [f"-I{d}" for d in inc] + [src, "-o", CALLS, "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
                                       "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:librglru.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -139,3 +139,68 @@ def test_outputs_apart_from_inputs():
     assert refused(lib.rglru_w4_linear(at(0), at(1), at(2), at(1), 2, 64, 64, 32, None))
     assert refused(lib.rglru_w4_glu(at(0), at(1), at(2), at(3), at(4), at(4), 2, 64, 64, 32, 0, None))
     assert refused(lib.rglru_w4_glu(at(0), at(1), at(2), at(3), at(4), at(3), 2, 64, 64, 32, 0, None))
+
+
+def _without_calls(monkeypatch):
+    import sys
+
+    import gated_linear_rnn_conv1d_b200 as package
+    monkeypatch.delattr(package, "_calls", raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._calls", None)  # its import fails
+    monkeypatch.setattr(_abi, "_calls", None)
+
+
+def test_binding_without_its_short_way(monkeypatch):
+    """A _calls.so that cannot be loaded costs a warning and time: the calls go the long way, which here finds CPU tensors."""
+    _without_calls(monkeypatch)
+    b = torch.bfloat16
+    w, x = torch.zeros(72, 64, dtype=b), torch.zeros(3, 64, dtype=b)
+    with pytest.warns(RuntimeWarning, match="_calls.so"):
+        with pytest.raises(ValueError, match="CUDA"):
+            rglru.glu_forward(w, w, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        rglru.act8_pack(x)
+
+
+@pytest.mark.gpu
+def test_long_way_gives_the_same(monkeypatch):
+    g = torch.Generator("cpu").manual_seed(1)
+    b = torch.bfloat16
+    W, x, dh = (torch.randn(*s, generator=g).to(b).to("cuda") for s in ((72, 64), (40, 64), (40, 72)))
+    q = rglru.w4_quantize(W, 64)
+
+    def work():
+        a = rglru.act8_pack(x)
+        r = rglru.glu_backward(W, W, x, dh, want_h=True)
+        return [rglru.glu_forward(W, W, x), *r.values(), rglru.glu_backward(W, W, a, dh)["dx"], a.codes, a.scales,
+                rglru.act8_unpack(a), rglru.w4_linear(q, x), rglru.w4_glu(q, q, x)]
+
+    want = work()
+    _without_calls(monkeypatch)
+    with pytest.warns(RuntimeWarning, match="_calls.so"):
+        got = work()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_build_without_pytorch(monkeypatch, tmp_path, capsys):
+    """librglru.so needs nvcc alone; without PyTorch or g++ the short way is left out, with a line that says so."""
+    import builtins
+    import shutil
+
+    from gated_linear_rnn_conv1d_b200 import build
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    real = builtins.__import__
+
+    def without_torch(name, *args, **kwargs):
+        if name == "torch":
+            raise ImportError(name)
+        return real(name, *args, **kwargs)
+
+    with monkeypatch.context() as m:
+        m.setattr(builtins, "__import__", without_torch)
+        build._build_calls(True)
+    assert "PyTorch" in capsys.readouterr().err
+    monkeypatch.setattr(shutil, "which", lambda name: None)
+    build._build_calls(True)
+    assert "g++" in capsys.readouterr().err
+    assert not (tmp_path / "_calls.so").exists()
