@@ -204,3 +204,25 @@ def test_backward_with_masked_channels_of_the_lowest_number():
     keep[32:64] = False
     assert torch.isfinite(r["dx"]).all() and torch.isfinite(r["h"]).all()
     assert torch.isfinite(r["dW_gate"][:, keep]).all() and torch.isfinite(r["dW_up"][:, keep]).all()
+
+
+def test_rglru_backward_at_the_values_of_a_checkpoint():
+    """The RG-LRU's backward from a checkpoint against the float64 oracle's at x̂, which the oracle forms from x itself;
+    tolerances as of the backward's own tests."""
+    import oracle
+    from gated_linear_rnn_conv1d_b200 import inputs
+    from test_gpu_backward import _tol
+    w = inputs.make_forward(2, 70, 136, BF, seed=5)
+    p = rglru.Params.from_host(w.params)
+    codes, scales = ff.act8_pack(f64(w.x).reshape(140, 136))
+    xhat = ff.act8_unpack(codes, scales).reshape(2, 70, 136)
+    kept = rglru.act8_unpack(rglru.act8_pack(w.x.to(DEV)))
+    y, _, _ = rglru.forward(p, kept)
+    dy = torch.randn(2, 70, 136, generator=torch.Generator("cpu").manual_seed(6)).to(BF)
+    got = rglru.backward(p, kept, y, dy.to(DEV))
+    ref = oracle.rglru_backward(xhat, w.params.conv_w, w.params.conv_b, w.params.W_a, w.params.b_a, w.params.W_x,
+                                w.params.b_x, w.params.Lambda, dy)
+    for k, v in ref.items():
+        err = oracle.max_rel_error(f64(got[k]), v)
+        print(f"{k}: {err:.2e}")
+        assert err <= _tol(k), k

@@ -455,3 +455,83 @@ def test_tails_of_the_activation(N, act):
     check("h again", r["h"][:, 0], a, np.abs(a))
     check("du", r["dx"][:, 1], a, np.abs(a))
     check("dg", r["dx"][:, 0], s, terms)
+
+
+def _at16(t=None, shape=None, dtype=BF):
+    """A tensor (a copy of t, or one to be filled) that starts 16 bytes past a 32-byte border, and a check that what lies
+    around it is as it was."""
+    shape = tuple(shape if t is None else t.shape)
+    n, off = int(np.prod(shape)), 16 // torch.empty(0, dtype=dtype).element_size()
+    buf = torch.full((n + 2048,), -7.0, dtype=dtype, device=DEV)
+    off += 1024
+    view = buf[off:off + n].view(shape)
+    assert view.data_ptr() % 32 == 16
+    if t is not None:
+        view.copy_(t)
+    return view, lambda: bool((buf[:off] == -7.0).all() and (buf[off + n:] == -7.0).all())
+
+
+# widths that are multiples of 16, whose rows start in the middle of a sector only because the buffer does; few tokens,
+# tiles, several tiles a pair, and one width that is no multiple of 16, whose rows change sides
+@pytest.mark.parametrize("N,D,H", [(5, 64, 272), (40, 136, 272), (300, 80, 528), (2100, 48, 2608), (130, 72, 264)])
+def test_forward_off_the_sectors(N, D, H):
+    x, Wg, Wu, _ = _draw(N, D, H, seed=N + 1)
+    want = rglru.glu_forward(Wg.to(DEV), Wu.to(DEV), x.to(DEV))
+    h, untouched = _at16(shape=(N, H))
+    rglru.glu_forward(*(_at16(t)[0] for t in (Wg, Wu, x)), h=h)
+    assert untouched() and torch.equal(h, want)
+    _check_forward(x, Wg, Wu, "gelu", h)
+
+
+# staged dW, rows stored by threads, sums in pieces, few tokens
+@pytest.mark.parametrize("N,D,H", [(40, 1088, 2608), (300, 144, 272), (5000, 48, 80), (40, 528, 2064), (7, 272, 528)])
+def test_backward_off_the_sectors(N, D, H):
+    x, Wg, Wu, dh = _draw(N, D, H, seed=N + 2)
+    dev = [t.to(DEV) for t in (Wg, Wu, x, dh)]
+    want = rglru.glu_backward(*dev, want_h=True)
+    _check_backward(x, Wg, Wu, dh, "gelu", want)
+    ws = torch.empty(rglru.glu_backward_workspace_bytes(N, D, H), dtype=torch.uint8, device=DEV)
+    shapes = {"dx": (N, D), "dW_gate": (H, D), "dW_up": (H, D), "h": (N, H)}
+    for moved in (*shapes, "all", "inputs too"):
+        out = {k: (_at16 if moved in (k, "all", "inputs too") else _guarded)(shape=s) for k, s in shapes.items()}
+        inputs = [_at16(t)[0] for t in dev] if moved == "inputs too" else dev
+        code = rglru._abi.load().rglru_glu_backward(
+            *(t.data_ptr() for t in inputs), *(out[k][0].data_ptr() for k in shapes), N, D, H, 0, ws.data_ptr(),
+            ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert code == 0 and rglru.workspace_status(None) == 0
+        assert all(untouched() for _, untouched in out.values()), moved
+        assert all(torch.equal(out[k][0], want[k]) for k in shapes), moved
+
+
+def test_others_off_the_sectors():
+    """The checkpoint and the 4-bit calls, their inputs and outputs 16 bytes past a 32-byte border."""
+    g = torch.Generator("cpu").manual_seed(3)
+    W = torch.randn(272, 128, generator=g).to(BF).to(DEV)
+    q = rglru.w4_quantize(W, 64)
+    again = rglru.w4_quantize(_at16(W)[0], 64)
+    assert torch.equal(q.codes, again.codes) and torch.equal(q.scales, again.scales)
+    moved = rglru.W4Weight(_at16_bytes(q.codes), _at16(q.scales)[0], 64)
+    for M in (1, 9, 40):
+        x = torch.randn(M, 128, generator=g).to(BF).to(DEV)
+        y, untouched = _at16(shape=(M, 272))
+        rglru.w4_linear(moved, _at16(x)[0], y=y)
+        assert untouched() and torch.equal(y, rglru.w4_linear(q, x))
+        h, untouched = _at16(shape=(M, 272))
+        rglru.w4_glu(moved, moved, _at16(x)[0], h=h)
+        assert untouched() and torch.equal(h, rglru.w4_glu(q, q, x))
+    for dtype in (BF, torch.float32):
+        for C in (64, 72):
+            x = torch.randn(9, C, generator=g).to(dtype).to(DEV)
+            want = rglru.act8_pack(x)
+            a = rglru.act8_pack(_at16(x, dtype=dtype)[0])
+            assert torch.equal(a.codes, want.codes) and torch.equal(a.scales, want.scales)
+            back, untouched = _at16(shape=(9, C), dtype=dtype)
+            rglru.act8_unpack(rglru.Act8(_at16_bytes(a.codes), _at16_bytes(a.scales), dtype), x=back)
+            assert untouched() and torch.equal(back, rglru.act8_unpack(want))
+
+
+def _at16_bytes(t):
+    buf = torch.empty(t.numel() + 64, dtype=t.dtype, device=DEV)
+    view = buf[16:16 + t.numel()].view(t.shape)
+    assert view.data_ptr() % 32 == 16
+    return view.copy_(t)
