@@ -1,6 +1,6 @@
 // Products of a few tokens (M ≤ 64) with weight matrices: y = x Wᵀ, or the gated pair
-// h = act(x W_gᵀ) ⊙ (x W_uᵀ), forward or with what its backward makes of g and u. What bounds them is the weights' way from HBM, each byte read once, so
-// the kernel is a stream of weights with the products on the side:
+// h = act(x W_gᵀ) ⊙ (x W_uᵀ), forward or with what its backward makes of g and u. Their floor is the weights' way from HBM,
+// each byte read once, so the kernel is a stream of weights with the products on the side:
 //
 // * 16 weight rows are a granule: in the gated form those of 8 channels, the gate's in rows 0–7 and the up
 //   projection's in 8–15, so that a thread ends with g and u of the same channel and token. A block has a
@@ -114,8 +114,8 @@ template <int GROUP> struct FewW4 {
   static constexpr int kRead = 4 * kWords;
   template <int SEG> static constexpr int kGroups = 2 * SEG / GROUP;  // of a row's segment
   static __device__ __forceinline__ int lane_k(int t) { return 8 * kWords * t; }
-  // Four bf16 pairs (k, k + 4), k = 0 … 3, of a word's eight weights, less 8: 0x4300 is 128, and four
-  // bits in the mantissa's last places make 128 + q.
+  // Four bf16 pairs (k, k + 4), k = 0 … 3, of a word's eight weights, less 8, by the widely published way of setting an
+  // exponent above small integers: 0x4300 is 128, and four bits in the mantissa's last places make 128 + q.
   static __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&p)[4]) {
     const __nv_bfloat162 bias = __floats2bfloat162_rn(136.0f, 136.0f);
 #pragma unroll

@@ -3,8 +3,9 @@
 //     g = x W_gᵀ,  u = x W_uᵀ,  h = act(g) ⊙ u,              x [N][D], W_g, W_u [H][D]
 //     dg = dh ⊙ u ⊙ act'(g),  du = dh ⊙ act(g)               (g and u formed again from x)
 //     dx = dg W_g + du W_u,   dW_g = dgᵀ x,  dW_u = duᵀ x.
-// Five products of 2·N·D·H operations or six halves of them: the tensor cores bound every part,
-// so the elementwise work rides in the products' epilogues and g, u are never stored.
+// The forward is two products of 2·N·D·H operations each, the backward six (g, u, two for dx, one for each dW). With many
+// tokens the tensor cores bound every part, so the elementwise work rides in the products' epilogues and g, u are never
+// stored.
 //
 // One kernel shape: persistent CTA pairs (cta_group::2) on output tiles of up to 256 × 256, as the gate
 // GEMM's: warp 0 loads by TMA, warp 1 of the leader issues the MMAs, eight warps of each CTA
@@ -677,7 +678,8 @@ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 // What a tile of so many k-blocks costs in k-blocks (of about 0.3 µs): its accumulator changes hands, and
 // where its k is short the epilogue is what it takes: twelve for 256 × 256 of dW stored by the threads, each a row of
 // its own, eight where they leave by TMA (D 4096, H 12288: 16 tokens 153 → 139 µs, 64 tokens 157 → 144, 256 tokens
-// 172 → 162; D 2048, H 6144: 44.8 → 40.0, 48.0 → 43.9, 55.3 → 51.6).
+// 172 → 162; D 2048, H 6144: 44.8 → 40.0, 48.0 → 43.9, 55.3 → 51.6; the shortest of several runs, their middle is up to
+// 15 % longer).
 int tile_cost(int k_blocks, int least) { return std::max(k_blocks + 2, least); }
 
 // The ring. A product's k-block has half_rows of A and b_bytes of B (multiples of 1024 bytes). Handing a stage over

@@ -1,9 +1,11 @@
 // Linears with 4-bit weights for a few tokens, for serving: y = x Ŵᵀ and the gated pair
 // h = act(x Ŵ_gᵀ) ⊙ (x Ŵ_uᵀ), x [M][K] bf16 with M ≤ 64,
 //     Ŵ[n][k] = s[n][k / G] · (q[n][k] − 8),   q in 4 bits (even k in the low half of a byte), s bf16.
-// HBM's floor is half a byte a weight and 2 / G of scale. The kernel is few_tokens.cuh's; unpacking takes
-// eleven operations for eight weights and their products two, of 22 that the SMs issue: where each block has
-// enough rows that, not HBM, bounds it (3.4 TB/s for 52 MB).
+// HBM's floor is half a byte a weight and 2 / G of scale. The kernel is few_tokens.cuh's. Up to eight tokens latency
+// bounds it: 52 MB take 15.3 µs (3.4 TB/s; alone and cold 20.4, HBM at a third of its rate and the issue slots at 40 %:
+// 22 instructions a warp for 256 weights, eleven the unpacking and two the products, are 7.6 µs of them), and warps wait
+// for loads as much as for anything else; a ring of two steps has one in flight. More tokens than 16 cost more than
+// their bytes (16, 32 and 64 tokens 19, 36 and 67 µs; the bf16 block, with four times the bytes, 37, 44 and 52).
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -68,7 +70,8 @@ FewArgs few_args(const W4Matrix& w0, const W4Matrix& w1, const void* x, void* ou
   return a;
 }
 
-// Quantisation: a thread forms one group of one row. s = bf16(max |w| / 7), q = rint(w / s) + 8, the
+// Quantisation, once for a matrix: a thread forms one group of one row (12288 × 4096: 76 µs in groups of 128, 47 in groups
+// of 32, of 19 that HBM's rate asks for: neighbouring threads read a group's width apart). s = bf16(max |w| / 7), q = rint(w / s) + 8, the
 // divisions IEEE float32's; |w / s| ≤ 7·(1 + 2^-8), so q stays in 1 … 15 wherever s is a normal
 // number (below, it is held there). A group of zeros gets s = 0 and q = 8; one that holds an
 // infinity or a NaN gets s = NaN.

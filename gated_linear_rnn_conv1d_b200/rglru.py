@@ -774,7 +774,9 @@ def glu_backward(W_gate: torch.Tensor, W_up: torch.Tensor, x: Union[torch.Tensor
                  stream: Optional[torch.cuda.Stream] = None) -> dict:
     """rglru_glu_backward (x a tensor) or rglru_glu_backward_act8 (x a checkpoint of it): the
     gradients of a loss with ∂ℓ/∂h = dh for glu_forward(W_gate, W_up, x). Returns a dict with dx
-    [..., D], dW_gate and dW_up [H][D] and, with want_h, the forward's h [..., H] (else None), bf16."""
+    [..., D], dW_gate and dW_up [H][D] and, with want_h, the forward's h [..., H] (else None), bf16.
+    The gradients of the two pre-activations are rounded to bf16 on their way into dx and dW, whose
+    sums are float32: each is off by up to 2^-8 of itself, as the outputs are by their own rounding."""
     packed = isinstance(x, Act8)
     if stream is None and workspace is None:
         r = _abi.calls().glu_backward(W_gate, W_up, None if packed else x, x.codes if packed else None,

@@ -442,8 +442,10 @@ RGLRU_API int rglru_gemm_bf16(const void* A, const void* Bm, void* C, int64_t M,
  * projection, for training and serving:
  *     h = act(x W_gateᵀ) ⊙ (x W_upᵀ)
  * in one kernel; what a call of this section and of the two below writes may not overlap what it
- * reads or what else it writes (RGLRU_ERR_SHAPE). Both products stay on the chip in float32 until h is rounded to bf16, once. (The
- * Hawk layer's calls above keep their own sequence of kernels and roundings.)
+ * reads or what else it writes (RGLRU_ERR_SHAPE). Both products stay on the chip in float32 until h is
+ * rounded to bf16, once; act is formed in float32, off by about 2e-7 · |g| and, down to g = −13, by no
+ * more than 2e-4 of its value. (The Hawk layer's calls above keep their own sequence of kernels and
+ * roundings.)
  *   x             [N][D] bf16 (N tokens, any batch and time shape)
  *   W_gate, W_up  [H][D] bf16, row-major [out][in]
  *   h             [N][H] bf16
@@ -459,8 +461,9 @@ RGLRU_API int rglru_gemm_bf16(const void* A, const void* Bm, void* C, int64_t M,
  *   dh [N][H], dx [N][D], dW_gate and dW_up [H][D]: bf16, sums in float32
  *   h             [N][H] bf16 or NULL: the forward's h again, for the down projection's gradient
  *   workspace     at least rglru_glu_backward_workspace_bytes(N, D, H, 0) bytes, 256-byte aligned
- *                 (dg and du in bf16, their rows padded to 64 columns; where dx or dW is cut
- *                 along its sum, the pieces in float32); it needs no initialisation
+ *                 (dg and du rounded to bf16, the operands of dx and dW, their rows padded to 64
+ *                 columns; where dx or dW is cut along its sum, the pieces in float32); it needs no
+ *                 initialisation
  * rglru_glu_backward_act8: the same, x given as its 8-bit checkpoint (rglru_act8_pack): the
  *   gradients at x̂, which the tensor cores read without a further rounding. workspace: at least
  *   rglru_glu_backward_workspace_bytes(N, D, H, 1) bytes.
